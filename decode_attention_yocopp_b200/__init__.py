@@ -32,7 +32,9 @@ EXPORTS = ("yocopp_compose_append", "yocopp_decode_attn_workspace_size", "yocopp
            "yocopp_testing_set_decode_fault", "yocopp_decode_attn_static", "yocopp_decode_attn_partial",
            "yocopp_decode_combine", "yocopp_decode_attn_fused", "yocopp_set_decode_kernel",
            "yocopp_prefill_attn", "yocopp_prefill_compose_attn_workspace_size", "yocopp_prefill_compose_attn",
-           "yocopp_testing_set_decode_prefetch")
+           "yocopp_testing_set_decode_prefetch", "yocopp_chunk_attn_workspace_size", "yocopp_chunk_attn",
+           "yocopp_rope_compose_append", "yocopp_pages_workspace_size", "yocopp_pages_resize", "yocopp_pages_fork",
+           "yocopp_pages_compact")
 
 
 class yocopp_cache(ctypes.Structure):
@@ -40,6 +42,15 @@ class yocopp_cache(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("num_blocks", ctypes.c_int32)]
+
+
+ROPE_MAX_AXES, ROPE_MAX_PAIRS = 4, 64
+
+
+class yocopp_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("axis", ctypes.c_int32 * ROPE_MAX_PAIRS),
+                ("inv_freq", ctypes.c_double * ROPE_MAX_PAIRS)]
 
 
 class YocoppError(RuntimeError):
@@ -99,6 +110,22 @@ def load(path: Optional[str] = None):
     lib.yocopp_prefill_compose_attn.argtypes = [V, V, V, V, ctypes.POINTER(ctypes.c_float), ctypes.c_float, V,
                                                 ctypes.POINTER(yocopp_cache), V, V, I32, I64, I32, V, I32,
                                                 ctypes.c_float, V, I64, V]
+    CACHE = ctypes.POINTER(yocopp_cache)
+    lib.yocopp_chunk_attn_workspace_size.restype = I64
+    lib.yocopp_chunk_attn_workspace_size.argtypes = [CACHE, I32]
+    lib.yocopp_chunk_attn.restype = I32
+    lib.yocopp_chunk_attn.argtypes = [V, CACHE, V, V, I32, I64, I32, V, I32, V, I32, ctypes.c_float, V, I64, V]
+    lib.yocopp_rope_compose_append.restype = I32
+    lib.yocopp_rope_compose_append.argtypes = [V, V, V, V, ctypes.POINTER(ctypes.c_float), ctypes.c_float,
+                                               ctypes.POINTER(yocopp_rope), V, CACHE, V, V, V, I32, V, I32, I64, V]
+    lib.yocopp_pages_workspace_size.restype = I64
+    lib.yocopp_pages_workspace_size.argtypes = [CACHE, I32]
+    lib.yocopp_pages_resize.restype = I32
+    lib.yocopp_pages_resize.argtypes = [CACHE, I32, V, V, V, I32, V, V, I64, V]
+    lib.yocopp_pages_fork.restype = I32
+    lib.yocopp_pages_fork.argtypes = [CACHE, I32, V, V, V, V, I32, I32, V, V, I64, V]
+    lib.yocopp_pages_compact.restype = I32
+    lib.yocopp_pages_compact.argtypes = [CACHE, I32, V, V, V, I64, V]
     if path is None:
         _lib = lib
     return lib
@@ -284,6 +311,183 @@ def yocopp_prefill_compose_attn(K1, V1, Ki, Vi, alpha, lam: float, q, cache: yoc
                                             int(max_q), _ptr(out), int(hq), float(scale), _ptr(workspace),
                                             workspace.numel() * workspace.element_size(), _stream(stream))
     _check("yocopp_prefill_compose_attn", rc)
+
+
+def yocopp_chunk_attn_workspace_size(cache: yocopp_cache, num_q_heads: int) -> int:
+    n = load().yocopp_chunk_attn_workspace_size(ctypes.byref(cache), int(num_q_heads))
+    if n < 0:
+        raise YocoppError("yocopp_chunk_attn_workspace_size", n)
+    return int(n)
+
+
+def _rows_of(q, total_q, num_q_heads):
+    return q.shape[0] if total_q is None else total_q, q.shape[1] if num_q_heads is None else num_q_heads
+
+
+def _on_device(t, name) -> None:
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise TypeError(f"{name}: a tensor of the current CUDA device expected, got {t.device}")
+
+
+def _want(t, name, dtype) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name}: contiguous {dtype} expected, got {t.dtype}, strides {tuple(t.stride())}")
+    _on_device(t, name)
+
+
+def _want_like_cache(t, name, cache) -> None:
+    """A packed [rows][heads][head_dim] tensor of the cache's type."""
+    if t is None:
+        return
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or _dtype_code(t) != cache.dtype or not t.is_contiguous():
+        raise TypeError(f"{name}: contiguous [rows][heads][{cache.head_dim}] of the cache's type expected, got "
+                        f"{t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}")
+    _on_device(t, name)
+
+
+def yocopp_chunk_attn(q, cache: yocopp_cache, out, workspace, pos=None, cu_q=None, n_uniform: int = 0,
+                      total_q: Optional[int] = None, max_q: int = 0, tree_mask=None, window: int = 0,
+                      num_q_heads: Optional[int] = None, scale: float = 0.0, stream=None) -> None:
+    """Attention of new tokens q [total_q][hq][d] at cache positions pos[b] + j over the cache: causal, over the
+    last ``window`` positions, or, with ``tree_mask`` (int64 [total_q], bit c = the row sees the chunk's row c), over
+    everything cached before the chunk and the marked rows of it.  out like q."""
+    import torch
+    total_q, hq = _rows_of(q, total_q, num_q_heads)
+    _want_like_cache(q, "q", cache)
+    _want_like_cache(out, "out", cache)
+    if out.shape != q.shape:
+        raise TypeError(f"out: {tuple(q.shape)} expected, got {tuple(out.shape)}")
+    _want(pos, "pos", torch.int32)
+    _want(cu_q, "cu_q", torch.int32)
+    _want(tree_mask, "tree_mask", torch.int64)
+    rc = load().yocopp_chunk_attn(_ptr(q), ctypes.byref(cache), _ptr(pos), _ptr(cu_q), int(n_uniform), int(total_q),
+                                  int(max_q), _ptr(tree_mask), int(window), _ptr(out), int(hq), float(scale),
+                                  _ptr(workspace),
+                                  workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                  _stream(stream))
+    _check("yocopp_chunk_attn", rc)
+
+
+def alloc_chunk_workspace(cache: yocopp_cache, num_q_heads: int, device=None):
+    """A torch byte tensor large enough (and 256-byte aligned) for yocopp_chunk_attn; it needs no clearing."""
+    import torch
+    return torch.empty(yocopp_chunk_attn_workspace_size(cache, num_q_heads), dtype=torch.uint8, device=device or "cuda")
+
+
+def make_rope(rotary_dim: int, base: float = 10000.0, sections: Optional[Sequence[int]] = None,
+              interleaved: bool = False, inv_freq: Optional[Sequence[float]] = None,
+              axis: Optional[Sequence[int]] = None) -> yocopp_rope:
+    """Descriptor of rotary positions.
+
+    Pair c (of rotary_dim / 2) turns by position * inv_freq[c], by default base ** (-2 c / rotary_dim).  sections:
+    how many consecutive pairs each axis has (default: one axis); axis: each pair's axis instead, in any order."""
+    pairs = rotary_dim // 2
+    if rotary_dim % 2 or not 1 <= pairs <= ROPE_MAX_PAIRS:
+        raise ValueError(f"rotary_dim {rotary_dim}: an even number from 2 to {2 * ROPE_MAX_PAIRS} expected")
+    if axis is None:
+        axis = [a for a, n in enumerate(sections if sections is not None else [pairs]) for _ in range(n)]
+    elif sections is not None:
+        raise ValueError("sections or axis, not both")
+    if inv_freq is None:
+        inv_freq = [float(base) ** (-2.0 * c / rotary_dim) for c in range(pairs)]
+    if len(axis) != pairs or len(inv_freq) != pairs:
+        raise ValueError(f"{pairs} pairs, but {len(axis)} axes and {len(inv_freq)} frequencies")
+    r = yocopp_rope()
+    r.rotary_dim, r.interleaved = rotary_dim, 1 if interleaved else 0
+    r.num_axes = max(len(sections) if sections is not None else 1, max(axis) + 1)
+    for c in range(pairs):
+        r.axis[c], r.inv_freq[c] = int(axis[c]), float(inv_freq[c])
+    return r
+
+
+def yocopp_rope_compose_append(K1, V1, Ki, Vi, alpha: Optional[Sequence[float]], lam: float, rope: yocopp_rope,
+                               positions, cache: yocopp_cache, pos, q=None, q_out=None, cu_new=None,
+                               n_uniform: int = 0, total_new: Optional[int] = None, stream=None) -> None:
+    """yocopp_compose_append with the keys turned by their tokens' positions (int32 [num_axes][total_new]), and the
+    queries q [total_new][hq][d] turned into q_out (which may be q).  K1 = V1 = Ki = Vi = None: queries only."""
+    import torch
+    a = None if alpha is None else (ctypes.c_float * 4)(*[float(x) for x in alpha])
+    if total_new is None:
+        total_new = K1.shape[0] if K1 is not None else q.shape[0] if q is not None else 0
+    for name, t in (("K1", K1), ("V1", V1), ("Ki", Ki), ("Vi", Vi), ("q", q), ("q_out", q_out)):
+        _want_like_cache(t, name, cache)
+        if t is not None and t.shape[0] != total_new:
+            raise TypeError(f"{name}: {total_new} rows expected, got {t.shape[0]}")
+    if q is not None and q_out is not None and q.shape != q_out.shape:
+        raise TypeError(f"q_out: {tuple(q.shape)} expected, got {tuple(q_out.shape)}")
+    if positions is not None and tuple(positions.shape) != (rope.num_axes, total_new):
+        raise TypeError(f"positions: [{rope.num_axes}][{total_new}] expected, got {tuple(positions.shape)}")
+    _want(positions, "positions", torch.int32)
+    _want(pos, "pos", torch.int32)
+    _want(cu_new, "cu_new", torch.int32)
+    rc = load().yocopp_rope_compose_append(_ptr(K1), _ptr(V1), _ptr(Ki), _ptr(Vi), a, float(lam), ctypes.byref(rope),
+                                           _ptr(positions), ctypes.byref(cache), _ptr(pos), _ptr(q), _ptr(q_out),
+                                           int(q.shape[1]) if q is not None else 0, _ptr(cu_new), int(n_uniform),
+                                           int(total_new), _stream(stream))
+    _check("yocopp_rope_compose_append", rc)
+
+
+def cache_list(caches: Sequence[yocopp_cache]):
+    """The descriptors of all layers' caches over one block table, as the page operators take them."""
+    c = (yocopp_cache * len(caches))(*caches)
+    c._keep = list(caches)  # keep the tensors alive with the descriptors
+    return c
+
+
+def yocopp_pages_workspace_size(caches) -> int:
+    n = load().yocopp_pages_workspace_size(caches, len(caches))
+    if n < 0:
+        raise YocoppError("yocopp_pages_workspace_size", n)
+    return int(n)
+
+
+def alloc_pages_workspace(caches, device=None):
+    """A torch byte tensor large enough (and 256-byte aligned) for the page operators; it needs no clearing."""
+    import torch
+    return torch.empty(yocopp_pages_workspace_size(caches), dtype=torch.uint8, device=device or "cuda")
+
+
+def _pages_args(caches, refs, workspace, **requests) -> int:
+    import torch
+    _want(refs, "refs", torch.int32)
+    if refs is not None and refs.numel() != caches[0].num_blocks:
+        raise TypeError(f"refs: {caches[0].num_blocks} counts expected, got {refs.numel()}")
+    n = min((t.numel() for t in requests.values()), default=0)
+    for name, t in requests.items():
+        _want(t, name, torch.int32)
+        if t.numel() != n:
+            raise TypeError(f"{name}: {n} entries expected, got {t.numel()}")
+    return n
+
+
+def yocopp_pages_resize(caches, refs, seqs, lens, held, workspace, stream=None) -> None:
+    """Table row seqs[i] is to hold lens[i] tokens: blocks are added or taken back, and a shared last block that is
+    kept in part is replaced by a copy.  held[i] = the blocks it holds then, or -1 where there were too few."""
+    n = _pages_args(caches, refs, workspace, seqs=seqs, lens=lens, held=held)
+    rc = load().yocopp_pages_resize(caches, len(caches), _ptr(refs), _ptr(seqs), _ptr(lens), n, _ptr(held),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("yocopp_pages_resize", rc)
+
+
+def yocopp_pages_fork(caches, refs, src, dst, lens, held, workspace, deep: bool = False, stream=None) -> None:
+    """Empty table row dst[i] gets the first lens[i] tokens of row src[i]: full blocks shared and a part of one
+    copied, or (deep) all copied."""
+    n = _pages_args(caches, refs, workspace, src=src, dst=dst, lens=lens, held=held)
+    rc = load().yocopp_pages_fork(caches, len(caches), _ptr(refs), _ptr(src), _ptr(dst), _ptr(lens), n,
+                                  1 if deep else 0, _ptr(held), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("yocopp_pages_fork", rc)
+
+
+def yocopp_pages_compact(caches, refs, live, workspace, stream=None) -> None:
+    """Move the blocks in use to the front of every layer's pool; live[0] = how many there are."""
+    _pages_args(caches, refs, workspace, live=live)
+    rc = load().yocopp_pages_compact(caches, len(caches), _ptr(refs), _ptr(live), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("yocopp_pages_compact", rc)
 
 
 STATIC_SCRATCH_BYTES = 4 << 20  # size of the library's fixed scratch array (include/yocopp.h)

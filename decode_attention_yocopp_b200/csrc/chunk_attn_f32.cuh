@@ -1,0 +1,404 @@
+// Attention of a chunk of new tokens over a cache, fp32, on the CUDA cores
+// (chunk_plan.cuh has the split of the work over the CTAs).
+//
+// A row tile is 64 rows (query heads of new tokens of one KV head) by key tiles
+// of 64 positions.  The 256 computing threads form a 16 x 16 grid: thread
+// (ty, tx) owns rows 4 ty .. +3 and keys tx, tx + 16, ... of the scores, and of
+// the output the same rows and the 16-byte channel chunks tx, tx + 16.  Both
+// products are packed fp32 FMAs (two channels at a time); 4 x 4 scores per
+// thread take 8 128-bit shared loads per 32 of them, which the shared memory
+// serves in less time than the FMA units need.  K and V tiles arrive by TMA
+// with a 128-byte swizzle, which spreads the 16 key rows a warp reads over all
+// banks.  Bound by the FMA units: 64 x 64 x 2 D multiply-adds per tile.
+//
+// C = 4 (at most 16 rows): the 16 rows are held four times and copy i takes
+// keys 16 i .. +15 of each tile, so that no multiply-add goes into empty rows;
+// the copies' results are merged at the end of a segment.
+//
+// Accuracy: scores, maxima, weights and sums in fp32, the value sum of a tile
+// formed by itself and then added to the running one (with the maximum's
+// correction in the same FMA), so that rounding grows with the number of tiles
+// and not of keys.
+#pragma once
+
+#include <type_traits>
+
+#include "chunk_plan.cuh"
+#include "decode_attn.cuh"
+
+namespace yocopp {
+
+template <int D, int C>
+struct ChunkF32 {
+    static constexpr int TK = 64, ROWS = 64, RT = ROWS / C;
+    static constexpr int NBOX = D / 32, BOXB = TK * 128, TILE_BYTES = NBOX * BOXB;
+    static constexpr int STAGES = 2, STAGE_BYTES = 2 * TILE_BYTES;
+    static constexpr int QS = D + 4, PS = TK + 4;  // padded row strides in floats
+    static constexpr int Q_OFF = STAGES * STAGE_BYTES;
+    static constexpr int P_OFF = Q_OFF + ROWS * QS * 4;
+    static constexpr int ML_OFF = P_OFF + ROWS * PS * 4;
+    static constexpr int BAR_OFF = ML_OFF + 2 * ROWS * 4;
+    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 1) * 8;
+    static constexpr int CTAS_PER_SM = D == 64 ? 2 : 1;
+    static constexpr int THREADS = 288;  // 8 computing warps and the loader
+};
+
+template <int D, int C>
+__global__ void __launch_bounds__(ChunkF32<D, C>::THREADS, ChunkF32<D, C>::CTAS_PER_SM)
+chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ ChunkParams p) {
+    using S = ChunkF32<D, C>;
+    constexpr int TK = S::TK, RT = S::RT, KP = 4 / C, CPT = D / 64;  // keys and channel chunks of a thread
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ volatile int s_abort;
+    __shared__ int64_t s_scan[S::THREADS / 32];
+    __shared__ ChunkStart s_start;
+
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x;
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* sQ = reinterpret_cast<float*>(base + S::Q_OFF);
+    float* sP = reinterpret_cast<float*>(base + S::P_OFF);
+    float* s_m = reinterpret_cast<float*>(base + S::ML_OFF);
+    float* s_l = s_m + S::ROWS;
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + S::BAR_OFF);
+    uint64_t* empty = full + S::STAGES;
+    uint64_t* merge_bar = empty + S::STAGES;
+    if (tid == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 8);
+        }
+        mbar_init(merge_bar, 8);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    chunk_find_start<RT, TK>(p, cta, s_scan, &s_start);
+    if (s_start.item >= s_start.end) {
+        if (tid == 0) __stcg(&p.desc[cta].last_cta, -1);
+        return;
+    }
+    ChunkWalk<RT, TK> walk(p, s_start);
+    ChunkSegment g;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------------ loader
+        if (lane == 0) {
+            const int nsb = TK / p.boxr;
+            int issued = 0;
+            bool ok = true;
+            prefetch_tensormap(&tmK);
+            prefetch_tensormap(&tmV);
+            while (ok && walk.next(g)) {
+                const int plane_row = (g.b * p.hkv + g.g) * p.capacity;
+                for (int t = g.t0; t < g.t1; ++t) {
+                    const int slot = issued % S::STAGES;
+                    int rows[TK / 16], nb = 0;
+#pragma unroll
+                    for (int sb = 0; sb < TK / 16; ++sb) {
+                        rows[sb] = -1;
+                        const int at = t * TK + sb * p.boxr;
+                        if (sb < nsb && at <= g.span.hi && at + p.boxr > g.span.lo) {
+                            if (p.block_table == nullptr) {
+                                rows[sb] = plane_row + at;
+                            } else {
+                                const int blk = __ldg(p.block_table + int64_t(g.b) * p.mbps + at / p.block_size);
+                                if (blk < 0 || blk >= p.num_blocks)
+                                    record_status(YOCOPP_EDEVICE_CHECK);
+                                else
+                                    rows[sb] = (blk * p.hkv + g.g) * p.block_size + at % p.block_size;
+                            }
+                            nb += rows[sb] >= 0;
+                        }
+                    }
+                    if (s_abort || !mbar_wait(&empty[slot], ((issued / S::STAGES) & 1) ^ 1, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const bool drop = cta == 0 && g.item + (t - g.t0) == p.drop_tile;  // failure injection (tests)
+                    if (!drop) mbar_arrive_expect_tx(&full[slot], uint32_t(2 * nb * p.boxr * 128 * S::NBOX));
+                    uint8_t* dst = base + slot * S::STAGE_BYTES;
+#pragma unroll
+                    for (int sb = 0; sb < TK / 16; ++sb) {
+                        if (rows[sb] < 0 || drop) continue;
+                        for (int bx = 0; bx < S::NBOX; ++bx) {
+                            tma_load_2d(dst + bx * S::BOXB + sb * p.boxr * 128, &tmK, &full[slot], bx * 32, rows[sb]);
+                            tma_load_2d(dst + S::TILE_BYTES + bx * S::BOXB + sb * p.boxr * 128, &tmV, &full[slot],
+                                        bx * 32, rows[sb]);
+                        }
+                    }
+                    ++issued;
+                }
+            }
+            if (!ok) {
+                record_status(YOCOPP_ETIMEOUT);
+                s_abort = 1;
+            }
+            if (!ok || s_abort)  // the copies in flight land before the CTA can exit
+                for (int t = max(0, issued - S::STAGES); t < issued; ++t)
+                    (void)mbar_wait(&full[t % S::STAGES], (t / S::STAGES) & 1, p.wait_limit_ns);
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------------ computing warps
+    const int ty = warp * 2 + (lane >> 4), tx = lane & 15;
+    const int copy = C == 1 ? 0 : ty / (16 / C);
+    const int lr0 = 4 * ty;                  // first of this thread's rows of the 64
+    const int row0 = lr0 % RT;               // the same in the row tile
+    int tiles = 0, merges = 0;
+    bool ok = true, split_end = false;
+    auto meet = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merge_bar);
+        return bool(__all_sync(0xffffffffu, mbar_wait(merge_bar, merges++ & 1, p.wait_limit_ns)));
+    };
+    while (walk.next(g)) {
+        const int64_t rows_all = int64_t(g.s.n) * p.G;
+        if (g.t0 == g.u0 && g.t1 < g.u1) {
+            split_end = true;
+            if (tid == 0) {
+                ChunkDesc* d = p.desc + cta;
+                __stcg(&d->row0, g.s.row0);
+                __stcg(&d->first_row, g.rt * RT);
+                __stcg(&d->rows, int(min(int64_t(RT), rows_all - int64_t(g.rt) * RT)));
+                __stcg(&d->g, g.g);
+                __stcg(&d->last_cta, chunk_cta_of(s_start.total, g.item + (g.u1 - g.u0) - 1, p.num_ctas));
+            }
+        }
+        // this warp's 8 rows of queries
+        {
+            constexpr int CH = D / 4;
+            __syncwarp();
+            for (int i = lane; i < 8 * CH; i += 32) {
+                const int lr = warp * 8 + i / CH, ch = i % CH;
+                const int R = g.rt * RT + lr % RT;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (R < rows_all) {
+                    const int j = R / p.G;
+                    v = ld_stream(p.q + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) * (D * 4) + ch * 16);
+                }
+                *reinterpret_cast<uint4*>(sQ + lr * S::QS + ch * 4) = v;
+            }
+            __syncwarp();
+        }
+        ChunkSight see[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            see[i] = chunk_sight(p, g.s, int(min(int64_t(g.rt * RT + row0 + i) / p.G, int64_t(g.s.n - 1))));
+        const int j0 = int(int64_t(g.rt) * RT / p.G);
+        const int j1 = int(min((int64_t(g.rt) * RT + RT - 1) / p.G, int64_t(g.s.n - 1)));
+        const int hi_all = p.tree ? g.s.p0 - 1 : g.s.p0 + j0;
+        const int lo_all = !p.tree && p.window ? max(0, g.s.p0 + j1 + 1 - p.window) : 0;
+        float m[4], l[4];
+        float2 o[4][2 * CPT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = NEG_INF_F;
+            l[i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2 * CPT; ++k) o[i][k] = make_float2(0.f, 0.f);
+        }
+        for (int t = g.t0; t < g.t1; ++t) {
+            const int slot = tiles % S::STAGES;
+            ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(&full[slot], (tiles / S::STAGES) & 1, p.wait_limit_ns));
+            if (!ok) break;
+            ++tiles;
+            const uint8_t* sK = base + slot * S::STAGE_BYTES;
+            const uint8_t* sV = sK + S::TILE_BYTES;
+            const int key0 = t * TK;
+            const bool masked = key0 + TK - 1 > hi_all || key0 < lo_all;
+            // ---- scores
+            float2 a[4][KP];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < KP; ++k) a[i][k] = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int ch = 0; ch < D / 4; ++ch) {
+                float4 q[4], kk[KP];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sQ + (lr0 + i) * S::QS + ch * 4);
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const int key = C == 1 ? tx + 16 * k : 16 * copy + tx;
+                    kk[k] = *reinterpret_cast<const float4*>(sK + (ch >> 3) * S::BOXB + key * 128 +
+                                                             (((ch & 7) ^ (key & 7)) << 4));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < KP; ++k) {
+                        a[i][k] = ffma2(make_float2(q[i].x, q[i].y), make_float2(kk[k].x, kk[k].y), a[i][k]);
+                        a[i][k] = ffma2(make_float2(q[i].z, q[i].w), make_float2(kk[k].z, kk[k].w), a[i][k]);
+                    }
+            }
+            // ---- weights against the running maximum
+            float corr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float s[KP], mx = NEG_INF_F;
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const int key = C == 1 ? tx + 16 * k : 16 * copy + tx;
+                    s[k] = (a[i][k].x + a[i][k].y) * p.qscale;
+                    if (masked && !see[i].sees(key0 + key)) s[k] = NEG_INF_F;
+                    mx = fmaxf(mx, s[k]);
+                }
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m[i], mx);
+                const float ref = mn == NEG_INF_F ? 0.f : mn;
+                corr[i] = m[i] == mn ? 1.f : exp2f(m[i] - mn);
+                m[i] = mn;
+                l[i] *= corr[i];
+#pragma unroll
+                for (int k = 0; k < KP; ++k) {
+                    const int key = C == 1 ? tx + 16 * k : 16 * copy + tx;
+                    const float e = exp2f(s[k] - ref);
+                    l[i] += e;
+                    sP[(lr0 + i) * S::PS + key] = e;
+                }
+            }
+            __syncwarp();
+            // ---- values
+            float2 w[4][2 * CPT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 2 * CPT; ++k) w[i][k] = make_float2(0.f, 0.f);
+            const int k0 = C == 1 ? 0 : 16 * copy;
+            auto values = [&](auto skip) {
+#pragma unroll 2
+                for (int kb = 0; kb < TK / C; kb += 4) {
+                    float4 pr[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        pr[i] = *reinterpret_cast<const float4*>(sP + (lr0 + i) * S::PS + k0 + kb);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const int key = k0 + kb + kk;
+                        float4 v[CPT];
+#pragma unroll
+                        for (int c = 0; c < CPT; ++c) {
+                            const int ch = tx + 16 * c;
+                            v[c] = *reinterpret_cast<const float4*>(sV + (ch >> 3) * S::BOXB + key * 128 +
+                                                                    (((ch & 7) ^ (key & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float e = reinterpret_cast<const float*>(&pr[i])[kk];
+                            if (decltype(skip)::value && e == 0.f) continue;  // a value that is not seen may be anything
+#pragma unroll
+                            for (int c = 0; c < CPT; ++c) {
+                                w[i][2 * c] = ffma2(make_float2(e, e), make_float2(v[c].x, v[c].y), w[i][2 * c]);
+                                w[i][2 * c + 1] = ffma2(make_float2(e, e), make_float2(v[c].z, v[c].w), w[i][2 * c + 1]);
+                            }
+                        }
+                    }
+                }
+            };
+            if (masked) values(std::true_type{});
+            else values(std::false_type{});
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 2 * CPT; ++k) o[i][k] = ffma2(o[i][k], make_float2(corr[i], corr[i]), w[i][k]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+            if (l[i] != l[i] && m[i] == NEG_INF_F) m[i] = 0.f;  // a NaN score makes the row NaN
+        }
+        const bool whole = g.t0 == g.u0 && g.t1 == g.u1;
+        float* slot = chunk_slot<RT, D>(p, cta, g.t0 == g.u0 ? 1 : 0);
+        auto put = [&](int row, int ch, float4 v) {  // 16-byte chunk ch of a row of the row tile
+            const int R = g.rt * RT + row;
+            if (R >= rows_all) return;
+            if (whole) {
+                const int j = R / p.G;
+                *reinterpret_cast<float4*>(p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) *
+                                                       int64_t(D * 4) + ch * 16) = v;
+            } else {
+                __stcg(reinterpret_cast<float4*>(slot + int64_t(row) * D + ch * 4), v);
+            }
+        };
+        if constexpr (C == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool none = m[i] == NEG_INF_F;
+                const float w = !whole ? 1.f : none ? 0.f : 1.f / l[i];
+                if (!whole && tx == 0 && g.rt * RT + row0 + i < rows_all) {
+                    __stcg(slot + RT * D + row0 + i, m[i]);
+                    __stcg(slot + RT * D + RT + row0 + i, l[i]);
+                }
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)
+                    put(row0 + i, tx + 16 * c,
+                        none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : make_float4(o[i][2 * c].x * w, o[i][2 * c].y * w, o[i][2 * c + 1].x * w,
+                                           o[i][2 * c + 1].y * w));
+            }
+        } else {
+            if (tx == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s_m[lr0 + i] = m[i];
+                    s_l[lr0 + i] = l[i];
+                }
+            }
+            ok = meet();  // also: no warp reads its queries any more
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float M = NEG_INF_F, L = 0.f;
+#pragma unroll
+                for (int k = 0; k < C; ++k) M = fmaxf(M, s_m[RT * k + row0 + i]);
+#pragma unroll
+                for (int k = 0; k < C; ++k) {
+                    const float mk = s_m[RT * k + row0 + i];
+                    L += mk == NEG_INF_F ? 0.f : s_l[RT * k + row0 + i] * exp2f(mk - M);
+                }
+                const float w = m[i] == NEG_INF_F ? 0.f : exp2f(m[i] - M) * (whole ? 1.f / L : 1.f);
+                if (!whole && copy == 0 && tx == 0 && g.rt * RT + row0 + i < rows_all) {
+                    __stcg(slot + RT * D + row0 + i, M);
+                    __stcg(slot + RT * D + RT + row0 + i, L);
+                }
+#pragma unroll
+                for (int c = 0; c < CPT; ++c)
+                    *reinterpret_cast<float4*>(sQ + (lr0 + i) * S::QS + (tx + 16 * c) * 4) =
+                        make_float4(o[i][2 * c].x * w, o[i][2 * c].y * w, o[i][2 * c + 1].x * w, o[i][2 * c + 1].y * w);
+            }
+            ok = meet();
+            if (!ok) break;
+            for (int i = tid; i < RT * (D / 4); i += 256) {
+                const int row = i / (D / 4), ch = i % (D / 4);
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < C; ++k) {
+                    const float4 b = *reinterpret_cast<const float4*>(sQ + (RT * k + row) * S::QS + ch * 4);
+                    s.x += b.x;
+                    s.y += b.y;
+                    s.z += b.z;
+                    s.w += b.w;
+                }
+                put(row, ch, s);
+            }
+            ok = meet();
+            if (!ok) break;
+        }
+    }
+    if (!ok) {
+        record_status(YOCOPP_ETIMEOUT);
+        s_abort = 1;
+    }
+    if (tid == 0 && !split_end) __stcg(&p.desc[cta].last_cta, -1);
+}
+
+}  // namespace yocopp

@@ -1,0 +1,358 @@
+// Work plan of the chunk attention, shared by its kernels and the merge.
+//
+// The rows of sequence b and KV head g are its new tokens' query heads of that
+// group, row r = j G + (h mod G), cut into row tiles of RT rows; the keys that
+// any row of a tile may see are cut into key tiles of TK positions.  Every
+// (row tile, key tile) pair is one item.  The items of all sequences, in the
+// order (sequence, KV head, row tile, key tile), are dealt out to the CTAs in
+// equal contiguous ranges, so that one long sequence or many short ones fill
+// the GPU alike.  A CTA's range is a run of segments, each a range of key
+// tiles of one row tile.  A segment that is a whole row tile is written to the
+// output; of the others a CTA has at most two (the end of a row tile begun by
+// an earlier CTA and the start of one that a later CTA goes on with), whose
+// unnormalised results go to its two slots of the workspace, and a second
+// launch merges them.
+#pragma once
+
+#include "common.cuh"
+
+namespace yocopp {
+
+struct ChunkParams {
+    const uint8_t* q;            // [total_q][hq][D]
+    uint8_t* out;                // [total_q][hq][D]
+    const uint8_t* k;            // cache (the kernel that loads without TMA)
+    const uint8_t* v;
+    const int32_t* pos;          // [batch] cache position of the first row, or null (0)
+    const int32_t* cu_q;         // [batch + 1], or null (n_uniform rows each)
+    const int32_t* block_table;  // null: contiguous
+    const unsigned long long* tree;  // [total_q] visible chunk positions, or null (causal)
+    int64_t total_q;
+    int32_t n_uniform, max_q, window;
+    int32_t batch, hq, hkv, G, capacity;
+    int32_t block_size, mbps, num_blocks, boxr;
+    float qscale;                // softmax scale * log2(e)
+    int32_t num_ctas;
+    float* part;                 // [num_ctas][2][RT][D + 2]: o, then m, l
+    struct ChunkDesc* desc;      // [num_ctas]
+    uint64_t wait_limit_ns;
+    int32_t drop_tile;           // testing: item of CTA 0 whose K load is never issued (-1: none)
+};
+
+// What the merge needs of a row tile that its CTA began and did not finish.
+struct ChunkDesc {
+    int32_t row0, first_row, rows, g;  // first query row of the sequence, first row of the tile, rows in it, KV head
+    int32_t last_cta;                  // the CTA that ends it; -1: nothing to merge
+    int32_t pad[3];
+};
+
+struct ChunkSeq {
+    int row0, n, p0;
+};
+
+// Rows and first position of sequence b; n = 0 where they are not valid (recorded where `report`).
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool report) {
+    ChunkSeq s;
+    if (p.cu_q) {
+        s.row0 = __ldg(p.cu_q + b);
+        s.n = __ldg(p.cu_q + b + 1) - s.row0;
+    } else {
+        s.row0 = b * p.n_uniform;
+        s.n = p.n_uniform;
+    }
+    s.p0 = p.pos ? __ldg(p.pos + b) : 0;
+    int bad = 0;
+    if (s.row0 < 0 || s.n < 0 || int64_t(s.row0) + s.n > p.total_q) bad = YOCOPP_EDEVICE_CHECK;
+    else if (s.n > p.max_q || s.p0 < 0 || int64_t(s.p0) + s.n > p.capacity) bad = YOCOPP_ECAPACITY;
+    if (bad) {
+        if (report) record_status(bad);
+        s.n = 0;
+    }
+    return s;
+}
+
+// Positions [lo, hi] that the rows of a row tile may see.
+struct ChunkSpan {
+    int lo, hi;
+};
+template <int RT>
+__device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const ChunkSeq& s, int rt) {
+    ChunkSpan r;
+    if (p.tree) {
+        r.lo = 0;
+        r.hi = s.p0 + s.n - 1;
+    } else {
+        const int j0 = int(int64_t(rt) * RT / p.G), j1 = min(int((int64_t(rt) * RT + RT - 1) / p.G), s.n - 1);
+        r.lo = p.window ? max(0, s.p0 + j0 + 1 - p.window) : 0;
+        r.hi = s.p0 + j1;
+    }
+    return r;
+}
+template <int RT>
+__device__ __forceinline__ int chunk_row_tiles(const ChunkParams& p, const ChunkSeq& s) {
+    return int((int64_t(s.n) * p.G + RT - 1) / RT);
+}
+template <int RT, int TK>
+__device__ __forceinline__ int64_t chunk_items_per_head(const ChunkParams& p, const ChunkSeq& s) {
+    int64_t t = 0;
+    const int nrt = chunk_row_tiles<RT>(p, s);
+    for (int rt = 0; rt < nrt; ++rt) {
+        const ChunkSpan r = chunk_span<RT>(p, s, rt);
+        t += r.hi / TK - r.lo / TK + 1;
+    }
+    return t;
+}
+
+// One segment: key tiles [t0, t1) of row tile rt of (b, g), whose key tiles are [u0, u1).
+struct ChunkSegment {
+    ChunkSeq s;
+    ChunkSpan span;
+    int b, g, rt, t0, t1, u0, u1;
+    int64_t item;  // number of its first item
+};
+
+// The CTA's place in the plan: found once by the whole CTA, then walked by every role for itself.
+struct ChunkStart {
+    int b, g, rt, t;
+    int64_t item, end, total;
+};
+
+// first item of CTA c
+__device__ __forceinline__ int64_t chunk_first_item(int64_t total, int c, int num_ctas) {
+    return total / num_ctas * c + min(int64_t(c), total % num_ctas);
+}
+// the CTA that has an item
+__device__ __forceinline__ int chunk_cta_of(int64_t total, int64_t item, int num_ctas) {
+    const int64_t q = total / num_ctas, r = total % num_ctas;
+    return int(item < r * (q + 1) ? item / (q + 1) : r + (item - r * (q + 1)) / q);
+}
+
+// All threads of the CTA call it; `start` is shared memory.  scan: one int64 per warp, shared.
+template <int RT, int TK>
+__device__ __forceinline__ void chunk_find_start(const ChunkParams& p, int cta, int64_t* scan, ChunkStart* start) {
+    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
+    const int per = (p.batch + nthr - 1) / nthr;
+    const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += chunk_items_per_head<RT, TK>(p, chunk_seq(p, b, cta == 0)) * p.hkv;
+    int64_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (lane == 31) scan[warp] = sum;
+    __syncthreads();
+    int64_t before = sum - mine, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t w0 = chunk_first_item(total, cta, p.num_ctas), w1 = chunk_first_item(total, cta + 1, p.num_ctas);
+    if (w0 >= w1) {
+        if (tid == 0) {
+            start->item = start->end = 0;
+            start->total = total;
+        }
+    } else if (w0 >= before && w0 < before + mine) {
+        int64_t at = before;
+        for (int b = b0; b < b1; ++b) {
+            const ChunkSeq s = chunk_seq(p, b, false);
+            const int64_t per_head = chunk_items_per_head<RT, TK>(p, s);
+            if (w0 >= at + per_head * p.hkv) {
+                at += per_head * p.hkv;
+                continue;
+            }
+            const int g = int((w0 - at) / per_head);
+            int64_t rem = (w0 - at) - g * per_head;
+            int rt = 0;
+            for (;; ++rt) {
+                const ChunkSpan r = chunk_span<RT>(p, s, rt);
+                const int n = r.hi / TK - r.lo / TK + 1;
+                if (rem < n) {
+                    start->t = r.lo / TK + int(rem);
+                    break;
+                }
+                rem -= n;
+            }
+            start->b = b;
+            start->g = g;
+            start->rt = rt;
+            start->item = w0;
+            start->end = w1;
+            start->total = total;
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+template <int RT, int TK>
+struct ChunkWalk {
+    const ChunkParams& p;
+    ChunkStart at;
+    ChunkSeq s;
+    int nrt;
+    __device__ __forceinline__ ChunkWalk(const ChunkParams& pp, const ChunkStart& st) : p(pp), at(st) {
+        if (at.item < at.end) {
+            s = chunk_seq(p, at.b, false);
+            nrt = chunk_row_tiles<RT>(p, s);
+        }
+    }
+    // the next segment of this CTA, or false
+    __device__ __forceinline__ bool next(ChunkSegment& seg) {
+        if (at.item >= at.end) return false;
+        seg.s = s;
+        seg.span = chunk_span<RT>(p, s, at.rt);
+        seg.b = at.b;
+        seg.g = at.g;
+        seg.rt = at.rt;
+        seg.u0 = seg.span.lo / TK;
+        seg.u1 = seg.span.hi / TK + 1;
+        seg.t0 = at.t < 0 ? seg.u0 : at.t;
+        seg.t1 = int(min(int64_t(seg.u1), seg.t0 + (at.end - at.item)));
+        seg.item = at.item;
+        at.item += seg.t1 - seg.t0;
+        at.t = -1;
+        if (++at.rt == nrt) {
+            at.rt = 0;
+            if (++at.g == p.hkv) {
+                at.g = 0;
+                if (at.item < at.end) {
+                    do {
+                        ++at.b;
+                        s = chunk_seq(p, at.b, false);
+                    } while (s.n == 0);
+                    nrt = chunk_row_tiles<RT>(p, s);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// Query row j's bit pattern or window, and whether it sees position u.
+struct ChunkSight {
+    int lo, hi;                // causal / window: positions [lo, hi]
+    unsigned long long bits;   // tree: chunk positions
+    int p0, n;
+    bool tree;
+    __device__ __forceinline__ bool sees(int u) const {
+        if (!tree) return u >= lo && u <= hi;
+        const int c = u - p0;
+        return c < 0 || (c < n && ((bits >> c) & 1ull));
+    }
+};
+__device__ __forceinline__ ChunkSight chunk_sight(const ChunkParams& p, const ChunkSeq& s, int j) {
+    ChunkSight r;
+    r.tree = p.tree != nullptr;
+    r.p0 = s.p0;
+    r.n = s.n;
+    r.bits = r.tree ? __ldg(p.tree + s.row0 + j) : 0ull;
+    r.hi = r.tree ? s.p0 + s.n - 1 : s.p0 + j;
+    r.lo = !r.tree && p.window ? max(0, s.p0 + j + 1 - p.window) : 0;
+    return r;
+}
+
+// Cache row of position u of (b, g), or -1 where its block is not valid (recorded).
+__device__ __forceinline__ int64_t chunk_cache_row(const ChunkParams& p, int b, int g, int u) {
+    if (p.block_table == nullptr) return (int64_t(b) * p.hkv + g) * p.capacity + u;
+    const int blk = __ldg(p.block_table + int64_t(b) * p.mbps + u / p.block_size);
+    if (blk < 0 || blk >= p.num_blocks) {
+        record_status(YOCOPP_EDEVICE_CHECK);
+        return -1;
+    }
+    return (int64_t(blk) * p.hkv + g) * p.block_size + u % p.block_size;
+}
+
+// Slot of the workspace for a segment that is not a whole row tile: 0 where an earlier CTA began
+// the row tile, 1 where this one did.
+template <int RT, int D>
+__device__ __forceinline__ float* chunk_slot(const ChunkParams& p, int cta, int which) {
+    return p.part + (int64_t(cta) * 2 + which) * RT * (D + 2);
+}
+
+// Merge of the split row tiles: block (c, y) takes rows [y ROWS, ...) of the row tile that CTA c
+// began and did not finish, if there is one: the parts are CTA c's slot 1 and slot 0 of the CTAs
+// up to last_cta, merged exactly (out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i).
+constexpr int kChunkMergeRows = 8, kChunkMergeThreads = 256;
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kChunkMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int W = kChunkMergeThreads / 32, C = D / 32;
+    __shared__ float s_m[W], s_l[W], s_o[W][D];
+    griddep_wait();
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int last = __ldcg(&p.desc[c].last_cta);
+    if (last < 0) return;
+    const int rows = __ldcg(&p.desc[c].rows);
+    const int r0 = blockIdx.y * kChunkMergeRows;
+    if (r0 >= rows) return;
+    const int row0 = __ldcg(&p.desc[c].row0), first_row = __ldcg(&p.desc[c].first_row), g = __ldcg(&p.desc[c].g);
+    const int parts = last - c + 1;
+    auto part = [&](int i) { return chunk_slot<RT, D>(p, c + i, i == 0 ? 1 : 0); };
+    // parts [i0, i1) step `step` of row r by one warp: (m, l, o)
+    auto gather = [&](int r, int i0, int step, float& m, float& l, float (&o)[C]) {
+        m = __int_as_float(0xff800000);
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) o[k] = 0.f;
+        for (int i = i0; i < parts; i += step) {
+            const float* s = part(i);
+            const float mi = __ldcg(s + RT * D + r), li = __ldcg(s + RT * D + RT + r);
+            float x[C];
+#pragma unroll
+            for (int k = 0; k < C; ++k) x[k] = __ldcg(s + r * D + k * 32 + lane);
+            if (mi == __int_as_float(0xff800000)) continue;  // a part in which the row sees nothing
+            const float mn = fmaxf(m, mi);
+            const float a = exp2f(m - mn), e = exp2f(mi - mn);
+            m = mn;
+            l = l * a + li * e;
+#pragma unroll
+            for (int k = 0; k < C; ++k) o[k] = o[k] * a + x[k] * e;
+        }
+    };
+    auto store = [&](int r, float l, const float (&o)[C]) {
+        const int row = first_row + r;
+        const int64_t at = (int64_t(row0) + row / p.G) * p.hq + g * p.G + row % p.G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+            reinterpret_cast<T*>(p.out)[at * D + k * 32 + lane] = T(l == 0.f ? 0.f : o[k] * inv);
+    };
+    float m, l, o[C];
+    if (parts < 2 * W) {  // a warp for each row
+        const int r = r0 + warp;
+        if (r >= rows) return;
+        gather(r, 0, 1, m, l, o);
+        store(r, l, o);
+        return;
+    }
+    for (int r = r0; r < min(rows, r0 + kChunkMergeRows); ++r) {  // all warps for one row
+        gather(r, warp, W, m, l, o);
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_l[warp] = l;
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k) s_o[warp][k * 32 + lane] = o[k];
+        __syncthreads();
+        if (warp == 0) {
+            float M = s_m[0];
+            for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w]);
+            l = 0.f;
+#pragma unroll
+            for (int k = 0; k < C; ++k) o[k] = 0.f;
+            for (int w = 0; w < W; ++w) {
+                if (s_m[w] == __int_as_float(0xff800000)) continue;
+                const float e = exp2f(s_m[w] - M);
+                l += s_l[w] * e;
+#pragma unroll
+                for (int k = 0; k < C; ++k) o[k] += s_o[w][k * 32 + lane] * e;
+            }
+            store(r, l, o);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace yocopp

@@ -1,0 +1,415 @@
+// Pages of the paged caches: rows of the block table grown, cut and released,
+// forked (full pages shared or copied) and moved together, with a count of
+// references per block kept on the device.
+//
+// All layers' pools share one block table, so each operator is two launches:
+// a table kernel that settles the blocks (one cluster of CTAs, whose phases
+// are separated by cluster barriers) and writes a list of copies (source,
+// destination, rows) into the workspace, and a copy kernel that carries it out
+// in every layer.  Blocks are given out in ascending order of their number to
+// the requests in order, so the result does not depend on timing.
+//
+// Bound: the table kernel by latency (a few dependent passes over the
+// reference counts and rows, a few microseconds), the copy kernel by memory.
+#pragma once
+
+#include "common.cuh"
+
+namespace yocopp {
+
+constexpr int kPagesMaxLayers = 128;
+constexpr int kPagesThreads = 1024;
+constexpr int kPagesMaxRequests = 8192;  // = the largest batch
+constexpr int kPagesMaxCluster = 8;
+constexpr int kCopyThreads = 256;
+
+enum { kPagesResize = 0, kPagesFork = 1, kPagesCompact = 2 };
+
+struct PagesParams {
+    int32_t* table;        // [batch][mbps]
+    int32_t* refs;         // [num_blocks]
+    const int32_t* a;      // resize: rows; fork: source rows
+    const int32_t* b;      // fork: destination rows
+    const int32_t* lens;   // tokens
+    int32_t* held;         // [n], or the number of live blocks (compact)
+    int32_t n, deep;
+    int32_t batch, mbps, bs_log2, num_blocks;
+    // workspace
+    int32_t* count;        // [0] copies, [1] compact: live blocks, [2] compact: live blocks below that number
+    int32_t* totals;       // [kPagesMaxCluster] blocks counted by each CTA
+    int4* copies;          // [num_blocks] source, destination, rows
+    int32_t* order;        // [num_blocks] free blocks ascending (compact: holes ascending)
+    int32_t* order2;       // [num_blocks] compact: moved blocks ascending
+    int32_t* remap;        // [num_blocks] compact: new number of a block at or past the live count
+    int4* req;             // [n] have, need, want (-1: refused), first place in `order`
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Exclusive prefix sum over the block's threads; `total` gets the sum.
+template <typename I>
+__device__ __forceinline__ I block_scan(I x, I* warp_sums, I& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    I s = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = s;
+    __syncthreads();
+    const I w = warp_sums[lane];
+    I ws = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I y = __shfl_up_sync(0xffffffffu, ws, o);
+        if (lane >= o) ws += y;
+    }
+    total = __shfl_sync(0xffffffffu, ws, 31);
+    return s - x + __shfl_sync(0xffffffffu, ws - w, warp);
+}
+
+// Blocks that a row holds: its leading entries that are not negative, found by a 32-way search
+// (every entry behind the last held one is negative).
+__device__ __forceinline__ int row_held(const int32_t* row, int mbps) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = mbps;  // the answer is in [lo, hi]
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + lane * step;
+        const bool in = at < hi && __ldcg(row + at) >= 0;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        const int k = __popc(m);  // the probes that hold are the first k
+        if (k == 0) return lo;
+        const int nlo = lo + (k - 1) * step + 1;
+        hi = min(hi, lo + k * step);
+        lo = nlo;
+    }
+    return lo;
+}
+
+// The free (FREE) or used blocks of [0, num_blocks), counted by warps over contiguous segments.
+// body(id, rank) is called for every such block with its rank among them.  Two calls of the
+// pair count / visit; `before` is the number in front of this CTA's part.
+struct Segment {
+    int lo, hi;
+};
+__device__ __forceinline__ Segment warp_segment(int nb) {
+    const int warps = int(cluster_size()) * (kPagesThreads / 32);
+    const int w = int(cluster_rank()) * (kPagesThreads / 32) + (threadIdx.x >> 5);
+    const int per = ((nb + warps - 1) / warps + 31) & ~31;
+    return Segment{min(nb, w * per), min(nb, (w + 1) * per)};
+}
+template <bool FREE>
+__device__ __forceinline__ int count_segment(const int32_t* refs, Segment s) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int i = s.lo; i < s.hi; i += 32 * 8) {
+        int r[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int id = i + 32 * k + lane;
+            r[k] = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) n += FREE ? r[k] == 0 : r[k] > 0;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+// visit(id, is, rank): every block of the segment, whether it is one that counts, and how many count before it
+template <bool FREE, typename F>
+__device__ __forceinline__ void visit_segment(const int32_t* refs, Segment s, int before, F visit) {
+    const int lane = threadIdx.x & 31;
+    for (int i = s.lo; i < s.hi; i += 32) {
+        const int id = i + lane;
+        const int r = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
+        const bool is = FREE ? r == 0 : r > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        if (id < s.hi) visit(id, is, before + __popc(m & ((1u << lane) - 1u)));
+        before += __popc(m);
+    }
+}
+
+// Counts before each warp's segment: the block's scan of the warps' counts plus the counts of
+// the CTAs in front, which go through the workspace.  The cluster barrier is inside.
+__device__ __forceinline__ int cluster_before(int mine, int32_t* totals, int* warp_sums, int& total) {
+    int cta;
+    const int before = block_scan((threadIdx.x & 31) == 0 ? mine : 0, warp_sums, cta);
+    if (threadIdx.x == 0) __stcg(totals + cluster_rank(), cta);
+    cluster_sync();
+    int add = 0;
+    total = 0;
+    for (int r = 0; r < int(cluster_size()); ++r) {
+        const int t = __ldcg(totals + r);
+        if (r < int(cluster_rank())) add += t;
+        total += t;
+    }
+    return __shfl_sync(0xffffffffu, before, 0) + add;
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __grid_constant__ PagesParams p) {
+    __shared__ int first[OP == kPagesCompact ? 1 : kPagesMaxRequests];  // first request that names a row
+    __shared__ int warp_sums[32];
+    __shared__ int64_t warp_sums64[32];
+    griddep_launch_dependents();  // the copy kernel's CTAs may take their places; they wait for this kernel's end
+    griddep_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warps = int(cluster_size()) * (kPagesThreads / 32);
+    const int warp = int(cluster_rank()) * (kPagesThreads / 32) + (tid >> 5);
+    const bool lead = cluster_rank() == 0;
+    const int bs = 1 << p.bs_log2;
+    if (lead && tid == 0) __stcg(p.count, 0);
+
+    if constexpr (OP == kPagesCompact) {
+        const Segment seg = warp_segment(p.num_blocks);
+        int live;
+        const int before = cluster_before(count_segment<false>(p.refs, seg), p.totals, warp_sums, live);
+        // live blocks below `live`: counted up to there by the warp whose segment holds that place
+        if (live >= seg.lo && live < seg.hi) {
+            int below = before;
+            visit_segment<false>(p.refs, Segment{seg.lo, live}, before,
+                                 [&](int, bool is, int rank) { below = rank + is; });
+            // the last block visited by the highest lane has the count
+            below = __reduce_max_sync(0xffffffffu, below);
+            if (lane == 0) __stcg(p.count + 2, below);
+        } else if (live == p.num_blocks && lead && tid == 0) {
+            __stcg(p.count + 2, live);
+        }
+        if (lead && tid == 0) {
+            __stcg(p.count + 1, live);
+            p.held[0] = live;
+        }
+        cluster_sync();
+        const int below = __ldcg(p.count + 2);
+        const int moves = live - below;
+        visit_segment<false>(p.refs, seg, before, [&](int id, bool used, int rank) {
+            if (id < live) {
+                if (!used) __stcg(p.order + (id - rank), id);
+            } else {
+                if (used) __stcg(p.order2 + (rank - below), id);
+                else __stcg(p.remap + id, -1);
+            }
+        });
+        cluster_sync();
+        for (int k = warp * 32 + lane; k < moves; k += warps * 32) {
+            const int src = __ldcg(p.order2 + k), dst = __ldcg(p.order + k);
+            p.copies[k] = make_int4(src, dst, bs, 0);
+            p.refs[dst] = __ldcg(p.refs + src);
+            p.refs[src] = 0;
+            p.remap[src] = dst;
+        }
+        if (lead && tid == 0) __stcg(p.count, moves);
+        return;
+    } else {
+        // a row named by two requests belongs to the first
+        const int32_t* target = OP == kPagesFork ? p.b : p.a;
+        for (int i = tid; i < p.batch; i += kPagesThreads) first[i] = p.n;
+        __syncthreads();
+        for (int i = tid; i < p.n; i += kPagesThreads) {
+            const int r = __ldcg(target + i);
+            if (r >= 0 && r < p.batch) atomicMin(&first[r], i);
+        }
+        __syncthreads();
+        // each request by a warp: what its row holds and what it needs; resize releases what it no longer needs
+        for (int i = warp; i < p.n; i += warps) {
+            const int row = __ldcg(target + i), len = __ldcg(p.lens + i);
+            int4 q = make_int4(0, 0, -1, 0);
+            int bad = 0;
+            if (row < 0 || row >= p.batch || first[row] != i) bad = YOCOPP_EDEVICE_CHECK;
+            else if (len < 0 || int64_t(len) > int64_t(p.mbps) << p.bs_log2) bad = YOCOPP_ECAPACITY;
+            if (!bad) {
+                q.y = int((int64_t(len) + bs - 1) >> p.bs_log2);
+                int32_t* entries = p.table + int64_t(row) * p.mbps;
+                if constexpr (OP == kPagesResize) {
+                    q.x = row_held(entries, p.mbps);
+                    for (int e = q.y + lane; e < q.x; e += 32) {
+                        const int id = __ldcg(entries + e);
+                        if (id < 0 || id >= p.num_blocks) {
+                            record_status(YOCOPP_EDEVICE_CHECK);
+                        } else if (atomicSub(p.refs + id, 1) <= 0) {  // counted less often than it is named
+                            atomicAdd(p.refs + id, 1);
+                            record_status(YOCOPP_EDEVICE_CHECK);
+                        }
+                        __stcg(entries + e, -1);
+                    }
+                    q.z = max(0, q.y - q.x);
+                } else {
+                    const int src = __ldcg(p.a + i);
+                    if (src < 0 || src >= p.batch || src == row || __ldcg(entries) >= 0) {
+                        bad = YOCOPP_EDEVICE_CHECK;
+                    } else {
+                        q.x = row_held(p.table + int64_t(src) * p.mbps, p.mbps);
+                        if (q.y > q.x) bad = YOCOPP_ECAPACITY;
+                        else q.z = p.deep ? q.y : q.y - (len >> p.bs_log2);
+                    }
+                }
+            }
+            if (bad) {
+                q.z = -1;
+                if (lane == 0) record_status(bad);
+            }
+            if (lane == 0) __stcg(p.req + i, q);
+        }
+        cluster_sync();
+        // resize: a last page that is kept in part and still shared is replaced by a copy
+        if constexpr (OP == kPagesResize) {
+            for (int i = int(cluster_rank()) * kPagesThreads + tid; i < p.n; i += int(cluster_size()) * kPagesThreads) {
+                int4 q = __ldcg(p.req + i);
+                const int len = __ldcg(p.lens + i);
+                if (q.z >= 0 && (len & (bs - 1)) && q.y <= q.x) {
+                    const int id = __ldcg(p.table + int64_t(__ldcg(p.a + i)) * p.mbps + q.y - 1);
+                    if (id >= 0 && id < p.num_blocks && __ldcg(p.refs + id) > 1) {
+                        q.z = 1;
+                        __stcg(p.req + i, q);
+                    }
+                }
+            }
+        }
+        const Segment seg = warp_segment(p.num_blocks);
+        int spare;
+        const int before = cluster_before(count_segment<true>(p.refs, seg), p.totals, warp_sums, spare);
+        // every CTA sums the requests' wants in order (the first CTA writes their places)
+        int64_t run = 0;
+        for (int i0 = 0; i0 < p.n; i0 += kPagesThreads) {
+            const int i = i0 + tid;
+            int4 q = i < p.n ? __ldcg(p.req + i) : make_int4(0, 0, 0, 0);
+            int64_t sum;
+            const int64_t at = block_scan(int64_t(max(0, q.z)), warp_sums64, sum);
+            if (lead && i < p.n) {
+                const int64_t base = run + at;
+                // places past the spare blocks: refused
+                q.w = base + max(0, q.z) <= spare ? int(base) : -1;
+                __stcg(p.req + i, q);
+            }
+            run += sum;
+        }
+        const int want_all = int(min(run, int64_t(spare)));
+        if (before < want_all)
+            visit_segment<true>(p.refs, seg, before, [&](int id, bool is, int rank) {
+                if (is && rank < want_all) __stcg(p.order + rank, id);
+            });
+        cluster_sync();
+        for (int i = warp; i < p.n; i += warps) {
+            const int4 q = __ldcg(p.req + i);
+            const int len = __ldcg(p.lens + i);
+            const bool given = q.z == 0 || (q.z > 0 && q.w >= 0);
+            if (lane == 0) {
+                p.held[i] = given ? q.y : -1;
+                if (q.z > 0 && q.w < 0) record_status(YOCOPP_ECAPACITY);
+            }
+            if (!given) continue;
+            if constexpr (OP == kPagesResize) {
+                if (q.z == 0) continue;
+                int32_t* entries = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
+                if (q.y > q.x) {
+                    for (int k = lane; k < q.z; k += 32) {
+                        const int id = __ldcg(p.order + q.w + k);
+                        entries[q.x + k] = id;
+                        p.refs[id] = 1;
+                    }
+                } else if (lane == 0) {
+                    const int old = __ldcg(entries + q.y - 1), id = __ldcg(p.order + q.w);
+                    entries[q.y - 1] = id;
+                    p.refs[id] = 1;
+                    atomicSub(p.refs + old, 1);
+                    p.copies[atomicAdd(p.count, 1)] = make_int4(old, id, len & (bs - 1), 0);
+                }
+            } else {
+                const int32_t* from = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
+                int32_t* entries = p.table + int64_t(__ldcg(p.b + i)) * p.mbps;
+                const int shared = q.y - q.z;
+                for (int k = lane; k < q.y; k += 32) {
+                    int id = __ldcg(from + k);
+                    if (id < 0 || id >= p.num_blocks) {
+                        record_status(YOCOPP_EDEVICE_CHECK);
+                        id = -1;
+                    }
+                    if (k < shared) {
+                        if (id >= 0) atomicAdd(p.refs + id, 1);
+                        entries[k] = id;
+                    } else {
+                        const int at = q.w + k - shared, to = __ldcg(p.order + at);
+                        entries[k] = to;
+                        p.refs[to] = 1;
+                        p.copies[at] = make_int4(id < 0 ? to : id, to, id < 0 ? 0 : min(bs, len - (k << p.bs_log2)), 0);
+                    }
+                }
+                // the copies are the places given out: as many as the last request that got any
+                if (lane == 0 && q.z > 0) atomicMax(p.count, q.w + q.z);
+            }
+        }
+    }
+}
+
+struct CopyParams {
+    uint8_t* k[kPagesMaxLayers];
+    uint8_t* v[kPagesMaxLayers];
+    const int32_t* count;
+    const int4* copies;
+    int32_t* table;          // compact: rewritten through remap (null otherwise)
+    const int32_t* remap;
+    int64_t entries;         // batch * mbps
+    int32_t num_blocks, layers, hkv, bs_log2, rowb_log2;
+};
+
+// Rows [0, rows) of every head of block src to block dst, in every layer.  A block is hkv planes
+// of bs rows; it is cut into pieces of 16 KB, one per CTA and turn, four 16-byte chunks in flight
+// per thread; chunks of rows past the copied ones are skipped.
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
+    constexpr int U = 4, PIECE = U * kCopyThreads * 16;
+    griddep_wait();
+    if (p.table != nullptr) {
+        const int live = __ldcg(p.count + 1);
+        for (int64_t i = int64_t(blockIdx.x) * kCopyThreads + threadIdx.x; i < p.entries;
+             i += int64_t(gridDim.x) * kCopyThreads) {
+            const int id = __ldcg(p.table + i);
+            if (id < live) continue;  // also an entry that holds no block
+            const int to = id < p.num_blocks ? __ldcg(p.remap + id) : -1;
+            if (to >= 0) p.table[i] = to;
+            else record_status(YOCOPP_EDEVICE_CHECK);
+        }
+    }
+    const int n = __ldcg(p.count);
+    const int64_t block_bytes = int64_t(p.hkv) << (p.bs_log2 + p.rowb_log2);
+    const int pieces = int((block_bytes + PIECE - 1) / PIECE);
+    const int per_copy = pieces * 2 * p.layers;
+    const int row_mask = (1 << p.bs_log2) - 1;
+    for (int64_t w = blockIdx.x; w < int64_t(n) * per_copy; w += gridDim.x) {
+        const int i = int(w / per_copy), r = int(w % per_copy);
+        const int plane = r / pieces, piece = r % pieces;
+        const int4 cp = __ldcg(p.copies + i);
+        uint8_t* base = (plane & 1) ? p.v[plane >> 1] : p.k[plane >> 1];
+        const uint8_t* src = base + cp.x * block_bytes;
+        uint8_t* dst = base + cp.y * block_bytes;
+        uint4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t off = int64_t(piece) * PIECE + (u * kCopyThreads + int(threadIdx.x)) * 16;
+            if (off < block_bytes && (int(off >> p.rowb_log2) & row_mask) < cp.z) x[u] = ld_stream(src + off);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t off = int64_t(piece) * PIECE + (u * kCopyThreads + int(threadIdx.x)) * 16;
+            if (off < block_bytes && (int(off >> p.rowb_log2) & row_mask) < cp.z) st_global(dst + off, x[u]);
+        }
+    }
+}
+
+}  // namespace yocopp

@@ -1,0 +1,272 @@
+// Rotary positions of one to four axes, fused with the YOCO++ residual
+// composition and the cache append, and applied to the queries in the same
+// launch.
+//
+// A token of an image or a video has several positions (time, row, column).
+// Channel pair c of a head belongs to axis a(c) and turns by the angle
+// position[a(c)] * inv_freq[c]:
+//   (x_lo, x_hi) -> (x_lo cos - x_hi sin, x_hi cos + x_lo sin).
+// The turn is linear, so turning the composed key equals composing turned keys:
+//   R K' = R lambda (aK1 K_1 + aK2 K_i),
+// and the stored key is rounded once, after the turn (the composed key stays
+// in fp32 until then).  Values are composed exactly as by
+// yocopp_compose_append; channels past the rotary ones pass unturned.
+//
+// Angles.  A position of 2^20 and more times a frequency near 1 leaves no
+// correct digit of the fraction of a turn in fp32 (2^20 * 2^-24 of a radian and
+// more is lost), so the product with inv_freq / (2 pi) is taken in fp64, its
+// nearest whole number of turns subtracted there, and only the remainder, at
+// most half a turn, goes to sincospif: an error of a few 2^-24.
+//
+// Bound: memory.  Per token the launch reads four raw rows and the queries and
+// writes two rows and the queries once.  The sines of a token serve all of its
+// heads: a CTA first forms the table of a few tokens in shared memory, then
+// streams their rows in 16-byte chunks, a thread taking both chunks of a pair.
+#pragma once
+
+#include "compose_append.cuh"
+
+namespace yocopp {
+
+constexpr int kRopeMaxPairs = 64;
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;  // tokens of one table at most
+
+struct RopeParams {
+    ComposeParams c;             // raw rows, cache, positions in the cache, weights (c.k1 null: queries only)
+    const uint8_t* q;            // [total][hq][D], or null
+    uint8_t* qo;
+    const int32_t* positions;    // [axes][total]
+    int64_t total;
+    int32_t hq, pairs, tokens;   // tokens: tokens of one table in this launch
+    double turns[kRopeMaxPairs];  // inv_freq / (2 pi)
+    uint8_t axis[kRopeMaxPairs];
+};
+
+__device__ __forceinline__ float2 rotate1(float lo, float hi, float2 cs) {
+    return make_float2(fmaf(lo, cs.x, -hi * cs.y), fmaf(hi, cs.x, lo * cs.y));
+}
+
+template <typename T> struct Chunk16;  // 16 bytes of T as fp32
+template <> struct Chunk16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[8]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = bf16x2_to_float2(w[i]);
+            f[2 * i] = t.x;
+            f[2 * i + 1] = t.y;
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        return make_uint4(float2_to_bf16x2(f[0], f[1]), float2_to_bf16x2(f[2], f[3]), float2_to_bf16x2(f[4], f[5]),
+                          float2_to_bf16x2(f[6], f[7]));
+    }
+};
+template <> struct Chunk16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(uint4 v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+
+// fp32 composition of one 16-byte chunk (not rounded to the cache type)
+template <typename T>
+__device__ __forceinline__ void compose_f32(uint4 a1, uint4 ai, const ComposeCoef& c, float (&f)[Chunk16<T>::N]) {
+    float x1[Chunk16<T>::N], xi[Chunk16<T>::N];
+    Chunk16<T>::unpack(a1, x1);
+    Chunk16<T>::unpack(ai, xi);
+#pragma unroll
+    for (int k = 0; k < Chunk16<T>::N; k += 2) {
+        const float2 y = compose2(make_float2(x1[k], x1[k + 1]), make_float2(xi[k], xi[k + 1]), c.na1, c.na2, c.a1,
+                                  c.a2, c.lam, c.nlam);
+        f[k] = y.x;
+        f[k + 1] = y.y;
+    }
+}
+
+template <typename T> __device__ __forceinline__ float load1(const uint8_t* p);
+template <> __device__ __forceinline__ float load1<__nv_bfloat16>(const uint8_t* p) {
+    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+}
+template <> __device__ __forceinline__ float load1<float>(const uint8_t* p) { return *reinterpret_cast<const float*>(p); }
+template <typename T> __device__ __forceinline__ void store1(uint8_t* p, float x);
+template <> __device__ __forceinline__ void store1<__nv_bfloat16>(uint8_t* p, float x) {
+    *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ void store1<float>(uint8_t* p, float x) { *reinterpret_cast<float*>(p) = x; }
+
+// How the two channels of pair c lie in a row:
+//   kRopeHalves       (c, c + pairs), pairs a multiple of a chunk's elements: a
+//                     thread takes the two chunks that hold the same pairs;
+//   kRopeInterleaved  (2c, 2c + 1): a thread takes one chunk;
+//   kRopeAny          (c, c + pairs) for every other count: a thread takes a pair.
+enum { kRopeHalves = 0, kRopeInterleaved = 1, kRopeAny = 2 };
+
+template <typename T, int D, int LAYOUT>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int N = Chunk16<T>::N, ROWB = D * Elem<T>::kBytes, CPR = ROWB / 16;
+    __shared__ float2 tab[kRopeTokens][kRopeMaxPairs];
+    __shared__ int64_t dst_row[kRopeTokens];  // cache row of the token's first KV head, or -1
+    griddep_wait();
+    const int tid = threadIdx.x;
+    const ComposeParams& c = p.c;
+    const bool append = c.k1 != nullptr;
+    const int pairs = p.pairs;
+    const ComposeCoef ck = make_coef(c.ak1, c.ak2, c.lam), cv = make_coef(c.av1, c.av2, c.lam);
+    const int64_t head_rows = c.block_table == nullptr ? c.capacity : c.block_size;
+    // items of one row that is turned: pairs of chunks, chunks, or single pairs and channels
+    const int turned = LAYOUT == kRopeHalves ? pairs / N + (CPR - 2 * (pairs / N))
+                     : LAYOUT == kRopeInterleaved ? CPR : pairs + (D - 2 * pairs);
+    for (int64_t t0 = int64_t(blockIdx.x) * p.tokens; t0 < p.total; t0 += int64_t(gridDim.x) * p.tokens) {
+        const int nt = int(min(int64_t(p.tokens), p.total - t0));
+        for (int i = tid; i < nt * pairs; i += kRopeThreads) {
+            const int t = i / pairs, k = i % pairs;
+            const int x = __ldg(p.positions + int64_t(p.axis[k]) * p.total + t0 + t);
+            double turn = double(x) * p.turns[k];
+            turn -= rint(turn);
+            float s, co;
+            sincospif(float(2.0 * turn), &s, &co);
+            tab[t][k] = make_float2(co, s);
+        }
+        if (append && tid < nt) {
+            const int64_t tok = t0 + tid;
+            int b;
+            int64_t j;
+            if (c.cu_new == nullptr) {
+                b = int(tok / c.n_uniform);
+                j = tok - int64_t(b) * c.n_uniform;
+            } else {
+                int lo = 0, hi = c.batch;  // the largest b with cu[b] <= tok
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (__ldg(c.cu_new + mid) <= tok) lo = mid; else hi = mid;
+                }
+                b = lo;
+                j = tok - __ldg(c.cu_new + b);
+            }
+            const int64_t at = __ldg(c.pos + b) + j;
+            int64_t row = -1;
+            if (at < 0 || at >= c.capacity) {
+                record_status(YOCOPP_ECAPACITY);
+            } else if (c.block_table == nullptr) {
+                row = int64_t(b) * c.hkv * c.capacity + at;
+            } else {
+                const int blk = __ldg(c.block_table + int64_t(b) * c.mbps + (at >> c.bs_log2));
+                if (blk < 0 || blk >= c.num_blocks) record_status(YOCOPP_EDEVICE_CHECK);
+                else row = ((int64_t(blk) * c.hkv) << c.bs_log2) + (at & ((1 << c.bs_log2) - 1));
+            }
+            dst_row[tid] = row;
+        }
+        __syncthreads();
+
+        // one item of a turned row: load(offset) gives the chunk's fp32 values, store(offset, values) rounds them
+        auto turn_row = [&](int t, int item, auto load, auto store) {
+            if constexpr (LAYOUT == kRopeHalves) {
+                const int half = pairs / N;  // chunks of one half
+                float lo[N], hi[N];
+                if (item < half) {
+                    load(item * 16, lo);
+                    load((item + half) * 16, hi);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        const float2 y = rotate1(lo[k], hi[k], tab[t][item * N + k]);
+                        lo[k] = y.x;
+                        hi[k] = y.y;
+                    }
+                    store(item * 16, lo);
+                    store((item + half) * 16, hi);
+                } else {
+                    load((item + half) * 16, lo);
+                    store((item + half) * 16, lo);
+                }
+            } else {
+                float x[N];
+                load(item * 16, x);
+#pragma unroll
+                for (int k = 0; k < N; k += 2) {
+                    const int pr = (item * N + k) / 2;
+                    if (pr < pairs) {
+                        const float2 y = rotate1(x[k], x[k + 1], tab[t][pr]);
+                        x[k] = y.x;
+                        x[k + 1] = y.y;
+                    }
+                }
+                store(item * 16, x);
+            }
+        };
+        // the same for single elements (kRopeAny)
+        auto turn_any = [&](int t, int item, auto load, auto store) {
+            constexpr int E = Elem<T>::kBytes;
+            if (item < pairs) {
+                const float lo = load(item * E), hi = load((item + pairs) * E);
+                const float2 y = rotate1(lo, hi, tab[t][item]);
+                store(item * E, y.x);
+                store((item + pairs) * E, y.y);
+            } else {
+                store((item + pairs) * E, load((item + pairs) * E));
+            }
+        };
+
+        if (append) {
+            for (int i = tid; i < nt * c.hkv * turned; i += kRopeThreads) {
+                const int row = i / turned, item = i % turned;
+                const int t = row / c.hkv, h = row % c.hkv;
+                if (dst_row[t] < 0) continue;
+                const int64_t in = ((t0 + t) * c.hkv + h) * ROWB;
+                uint8_t* out = c.ck + (dst_row[t] + h * head_rows) * ROWB;
+                if constexpr (LAYOUT == kRopeAny) {
+                    turn_any(t, item,
+                             [&](int off) {
+                                 const float2 y = compose2(make_float2(load1<T>(c.k1 + in + off), 0.f),
+                                                           make_float2(load1<T>(c.ki + in + off), 0.f), ck.na1, ck.na2,
+                                                           ck.a1, ck.a2, ck.lam, ck.nlam);
+                                 return y.x;
+                             },
+                             [&](int off, float x) { store1<T>(out + off, x); });
+                } else {
+                    turn_row(t, item,
+                             [&](int off, float (&f)[N]) {
+                                 compose_f32<T>(ld_stream(c.k1 + in + off), ld_stream(c.ki + in + off), ck, f);
+                             },
+                             [&](int off, const float (&f)[N]) { st_global(out + off, Chunk16<T>::pack(f)); });
+                }
+            }
+            for (int i = tid; i < nt * c.hkv * CPR; i += kRopeThreads) {
+                const int row = i / CPR, off = (i % CPR) * 16;
+                const int t = row / c.hkv, h = row % c.hkv;
+                if (dst_row[t] < 0) continue;
+                const int64_t in = ((t0 + t) * c.hkv + h) * ROWB + off;
+                st_global(c.cv + (dst_row[t] + h * head_rows) * ROWB + off,
+                          compose_chunk<T>(ld_stream(c.v1 + in), ld_stream(c.vi + in), cv));
+            }
+        }
+        if (p.q != nullptr) {
+            // q may be turned in place: a thread reads all that it writes, and nobody else reads it
+            for (int i = tid; i < nt * p.hq * turned; i += kRopeThreads) {
+                const int row = i / turned, item = i % turned;
+                const int64_t in = (t0 * p.hq + row) * ROWB;
+                if constexpr (LAYOUT == kRopeAny) {
+                    turn_any(row / p.hq, item, [&](int off) { return load1<T>(p.q + in + off); },
+                             [&](int off, float x) { store1<T>(p.qo + in + off, x); });
+                } else {
+                    turn_row(row / p.hq, item,
+                             [&](int off, float (&f)[N]) {
+                                 Chunk16<T>::unpack(*reinterpret_cast<const uint4*>(p.q + in + off), f);
+                             },
+                             [&](int off, const float (&f)[N]) { st_global(p.qo + in + off, Chunk16<T>::pack(f)); });
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace yocopp

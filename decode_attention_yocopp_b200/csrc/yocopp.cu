@@ -1,18 +1,23 @@
 // yocopp C ABI: host-side argument checks, TMA descriptor encoding, split
-// planning and kernel launches for the YOCO++ compose/append and the shared-
-// cache decode attention.  One translation unit holds every kernel so the
-// device status word is a single symbol.
+// planning and kernel launches for the YOCO++ compose/append, the shared-
+// cache decode attention, the chunk attention, the rotary append and the page
+// operators.  One translation unit holds every kernel so the device status
+// word is a single symbol.
 #include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 
+#include "chunk_attn_f32.cuh"
+#include "chunk_attn_tc.cuh"
 #include "common.cuh"
 #include "compose_append.cuh"
 #include "decode_attn.cuh"
 #include "decode_attn_tc.cuh"
+#include "pages.cuh"
 #include "prefill_attn_tc.cuh"
+#include "rope_append.cuh"
 
 namespace yocopp {
 namespace {
@@ -310,6 +315,203 @@ int32_t check_decode_shape(const yocopp_cache* cache, int32_t num_q_heads, int* 
     const int64_t tiles = int64_t(cache->batch) * cache->num_kv_heads * ((cache->capacity + tile - 1) / tile);
     if (tiles >= (int64_t(1) << 31)) return YOCOPP_EINVAL;
     return YOCOPP_OK;
+}
+
+// ---------------------------------------------------------------- chunk attention
+// Launch with dynamic shared memory and as a programmatic dependent of the previous kernel.
+template <typename... P, typename... A>
+int32_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&lc, kern, args...));
+}
+
+// Workspace of the chunk attention: one descriptor per CTA, then two slots per CTA of rows x (D + 2) fp32.
+int64_t chunk_desc_bytes(int64_t ctas) { return int64_t(up256(size_t(ctas) * sizeof(ChunkDesc))); }
+int64_t chunk_slot_bytes(int rows, int D) { return int64_t(2) * rows * (D + 2) * int64_t(sizeof(float)); }
+
+// The widest of the launches that a cache and head count can get.
+int64_t chunk_workspace_bytes(const yocopp_cache* c, int sms) {
+    if (c->dtype == YOCOPP_BF16) return chunk_desc_bytes(sms) + sms * chunk_slot_bytes(256, c->head_dim);
+    const int64_t ctas = int64_t(sms) * (c->head_dim == 64 ? ChunkF32<64, 1>::CTAS_PER_SM : ChunkF32<128, 1>::CTAS_PER_SM);
+    return chunk_desc_bytes(ctas) + ctas * chunk_slot_bytes(64, c->head_dim);
+}
+
+template <typename S, typename T, int D, typename K>
+int32_t launch_chunk(K kern, const yocopp_cache* cache, ChunkParams& p, int64_t cache_rows, int rows, int ctas,
+                     void* workspace, cudaStream_t st) {
+    static bool attr_set[kMaxDevices] = {false};
+    const int dev = current_device();
+    if (dev < 0 || dev >= kMaxDevices) return YOCOPP_ECUDA;
+    if (!attr_set[dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
+            return YOCOPP_ECUDA;
+        attr_set[dev] = true;
+    }
+    p.boxr = cache->block_table ? (cache->block_size < S::TK ? cache->block_size : S::TK) : S::TK;
+    alignas(64) CUtensorMap tk, tv;
+    if (!encode_rows(&tk, cache->k, cache->dtype, D, cache_rows, p.boxr) ||
+        !encode_rows(&tv, cache->v, cache->dtype, D, cache_rows, p.boxr))
+        return YOCOPP_ECUDA;
+    p.num_ctas = ctas;
+    p.desc = static_cast<ChunkDesc*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + chunk_desc_bytes(ctas));
+    const int32_t rc = launch_dependent(kern, dim3(unsigned(ctas)), S::THREADS, S::SMEM, st, tk, tv, p);
+    if (rc != YOCOPP_OK) return rc;
+    const int most = rows < S::RT ? rows : S::RT;  // rows of the largest row tile
+    return launch_dependent(chunk_merge_kernel<T, D, S::RT>,
+                            dim3(unsigned(ctas), unsigned((most + kChunkMergeRows - 1) / kChunkMergeRows)),
+                            kChunkMergeThreads, 0, st, p);
+}
+
+template <int D>
+int32_t launch_chunk_any(const yocopp_cache* cache, ChunkParams& p, int64_t cache_rows, int rows, int sms,
+                         void* workspace, cudaStream_t st) {
+#define YOCOPP_CHUNK_TC(CC) \
+    return launch_chunk<ChunkTc<D, CC>, __nv_bfloat16, D>(chunk_tc_kernel<D, CC>, cache, p, cache_rows, rows, sms, workspace, st)
+#define YOCOPP_CHUNK_F32(CC)                                                                                     \
+    return launch_chunk<ChunkF32<D, CC>, float, D>(chunk_f32_kernel<D, CC>, cache, p, cache_rows, rows,          \
+                                                   sms * ChunkF32<D, CC>::CTAS_PER_SM, workspace, st)
+    if (cache->dtype == YOCOPP_BF16) {
+        if (rows <= 32) YOCOPP_CHUNK_TC(4);
+        if (rows <= 64) YOCOPP_CHUNK_TC(2);
+        if (rows <= 128) YOCOPP_CHUNK_TC(1);
+        YOCOPP_CHUNK_TC(0);
+    }
+    if (rows <= 16) YOCOPP_CHUNK_F32(4);
+    YOCOPP_CHUNK_F32(1);
+#undef YOCOPP_CHUNK_TC
+#undef YOCOPP_CHUNK_F32
+}
+
+// ---------------------------------------------------------------- rotary append
+template <typename T, int D>
+int32_t launch_rope(RopeParams& p, bool interleaved, int sms, cudaStream_t st) {
+    // tables of as many tokens as leave every SM two CTAs' worth, four at most
+    p.tokens = p.total >= int64_t(sms) * 8 ? kRopeTokens : 1;
+    int64_t grid = (p.total + p.tokens - 1) / p.tokens;
+    if (grid > int64_t(sms) * 8) grid = int64_t(sms) * 8;
+    const dim3 g{unsigned(grid)};
+    if (interleaved) return launch_dependent(rope_append_kernel<T, D, kRopeInterleaved>, g, kRopeThreads, 0, st, p);
+    if (p.pairs % Chunk16<T>::N == 0) return launch_dependent(rope_append_kernel<T, D, kRopeHalves>, g, kRopeThreads, 0, st, p);
+    return launch_dependent(rope_append_kernel<T, D, kRopeAny>, g, kRopeThreads, 0, st, p);
+}
+
+// ---------------------------------------------------------------- pages
+struct PagesLayout {
+    size_t count, totals, copies, order, order2, remap, req, bytes;
+};
+PagesLayout pages_layout(size_t num_blocks, size_t batch) {
+    PagesLayout w;
+    w.count = 0;
+    w.totals = 64;
+    w.copies = 256;
+    w.order = w.copies + up256(num_blocks * sizeof(int4));
+    w.order2 = w.order + up256(num_blocks * sizeof(int32_t));
+    w.remap = w.order2 + up256(num_blocks * sizeof(int32_t));
+    w.req = w.remap + up256(num_blocks * sizeof(int32_t));
+    w.bytes = w.req + up256(batch * sizeof(int4));
+    return w;
+}
+
+// The layers' caches of one block table: the same shape and type in each.
+int32_t check_pages(const yocopp_cache* c, int32_t num_caches) {
+    if (c == nullptr || num_caches < 1 || num_caches > kPagesMaxLayers) return YOCOPP_EINVAL;
+    for (int i = 0; i < num_caches; ++i) {
+        const int32_t rc = check_cache(c + i);
+        if (rc != YOCOPP_OK) return rc;
+        if (c[i].block_table == nullptr || c[i].block_table != c->block_table || c[i].dtype != c->dtype ||
+            c[i].batch != c->batch || c[i].num_kv_heads != c->num_kv_heads || c[i].head_dim != c->head_dim ||
+            c[i].block_size != c->block_size || c[i].max_blocks_per_seq != c->max_blocks_per_seq ||
+            c[i].num_blocks != c->num_blocks)
+            return YOCOPP_EINVAL;
+    }
+    if (!aligned(c->block_table, 4)) return YOCOPP_EINVAL;
+    return YOCOPP_OK;
+}
+
+int ilog2(int64_t x) {
+    int n = 0;
+    while ((int64_t(1) << n) < x) ++n;
+    return n;
+}
+
+// The table kernel (one cluster), then the copies in every layer.
+template <int OP>
+int32_t launch_pages(const yocopp_cache* caches, int32_t num_caches, PagesParams& p, void* workspace,
+                     int64_t workspace_bytes, cudaStream_t st) {
+    const yocopp_cache* c = caches;
+    const PagesLayout w = pages_layout(size_t(c->num_blocks), size_t(c->batch));
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < int64_t(w.bytes)) return YOCOPP_EWORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.table = const_cast<int32_t*>(c->block_table);
+    p.batch = c->batch;
+    p.mbps = c->max_blocks_per_seq;
+    p.bs_log2 = ilog2(c->block_size);
+    p.num_blocks = c->num_blocks;
+    p.count = reinterpret_cast<int32_t*>(ws + w.count);
+    p.totals = reinterpret_cast<int32_t*>(ws + w.totals);
+    p.copies = reinterpret_cast<int4*>(ws + w.copies);
+    p.order = reinterpret_cast<int32_t*>(ws + w.order);
+    p.order2 = reinterpret_cast<int32_t*>(ws + w.order2);
+    p.remap = reinterpret_cast<int32_t*>(ws + w.remap);
+    p.req = reinterpret_cast<int4*>(ws + w.req);
+
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return YOCOPP_ECUDA;
+    // one CTA settles small pools and few requests (a cluster barrier between CTAs costs more than it
+    // saves there); eight share large ones
+    const int cluster = c->num_blocks <= 8192 && (OP == kPagesCompact || p.n <= 32) ? 1 : kPagesMaxCluster;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(unsigned(cluster), 1, 1);
+    lc.blockDim = dim3(kPagesThreads, 1, 1);
+    lc.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 2;
+    const int32_t rc = cuda_status(cudaLaunchKernelEx(&lc, pages_table_kernel<OP>, p));
+    if (rc != YOCOPP_OK) return rc;
+
+    CopyParams q = {};
+    for (int i = 0; i < num_caches; ++i) {
+        q.k[i] = static_cast<uint8_t*>(caches[i].k);
+        q.v[i] = static_cast<uint8_t*>(caches[i].v);
+    }
+    q.count = p.count;
+    q.copies = p.copies;
+    q.table = OP == kPagesCompact ? p.table : nullptr;
+    q.remap = p.remap;
+    q.entries = int64_t(p.batch) * p.mbps;
+    q.num_blocks = p.num_blocks;
+    q.layers = num_caches;
+    q.hkv = c->num_kv_heads;
+    q.bs_log2 = p.bs_log2;
+    q.rowb_log2 = ilog2(c->head_dim * elem_bytes(c->dtype));
+    const int64_t block_bytes = int64_t(q.hkv) << (q.bs_log2 + q.rowb_log2);
+    const int64_t pieces = (block_bytes + 4 * kCopyThreads * 16 - 1) / (4 * kCopyThreads * 16) * 2 * num_caches;
+    // copies there can be: one per request (resize, shared fork), one per block otherwise
+    const int64_t copies = OP == kPagesResize || (OP == kPagesFork && !p.deep) ? p.n : p.num_blocks;
+    int64_t grid = pieces * copies;
+    if (OP == kPagesCompact) {
+        const int64_t rewrite = (q.entries + kCopyThreads - 1) / kCopyThreads;
+        if (grid < rewrite) grid = rewrite;
+    }
+    if (grid > int64_t(sms) * 8) grid = int64_t(sms) * 8;
+    return launch_dependent(pages_copy_kernel, dim3(unsigned(grid)), kCopyThreads, 0, st, q);
 }
 
 }  // namespace
@@ -783,6 +985,201 @@ int32_t yocopp_prefill_compose_attn(const void* K1, const void* V1, const void* 
     f.workspace = workspace;
     f.workspace_bytes = workspace_bytes;
     return prefill_attn_impl(q, cache, pos, cu_q, n_uniform, total_q, max_q, out, num_q_heads, scale, stream, &f);
+}
+
+int64_t yocopp_chunk_attn_workspace_size(const yocopp_cache* cache, int32_t num_q_heads) {
+    const int32_t rc = check_cache(cache);
+    if (rc != YOCOPP_OK) return rc;
+    if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0) return YOCOPP_EINVAL;
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return YOCOPP_ECUDA;
+    return chunk_workspace_bytes(cache, sms);
+}
+
+int32_t yocopp_chunk_attn(const void* q, const yocopp_cache* cache, const int32_t* pos, const int32_t* cu_q,
+                          int32_t n_uniform, int64_t total_q, int32_t max_q, const uint64_t* tree_mask,
+                          int32_t window, void* out, int32_t num_q_heads, float scale, void* workspace,
+                          int64_t workspace_bytes, void* stream) {
+    const int32_t rc = check_cache(cache);
+    if (rc != YOCOPP_OK) return rc;
+    if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0) return YOCOPP_EINVAL;
+    if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return YOCOPP_EINVAL;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return YOCOPP_EINVAL;
+    if (total_q < 0 || total_q >= (int64_t(1) << 31) || window < 0) return YOCOPP_EINVAL;
+    if (cu_q == nullptr) {
+        if (n_uniform < 0 || int64_t(n_uniform) * cache->batch != total_q) return YOCOPP_EINVAL;
+        max_q = n_uniform;
+    } else if (max_q < 0) {
+        return YOCOPP_EINVAL;
+    }
+    if (max_q > cache->capacity) return YOCOPP_EINVAL;
+    if (tree_mask != nullptr && (window != 0 || max_q > 64 || !aligned(tree_mask, 8))) return YOCOPP_EINVAL;
+    const int G = num_q_heads / cache->num_kv_heads;
+    if (int64_t(max_q) * G + 256 >= (int64_t(1) << 31)) return YOCOPP_EINVAL;  // rows of a sequence stay 32-bit
+    const bool paged = cache->block_table != nullptr;
+    const int64_t rows = paged ? int64_t(cache->num_blocks) * cache->num_kv_heads * cache->block_size
+                               : int64_t(cache->batch) * cache->num_kv_heads * cache->capacity;
+    if (rows + 128 >= (int64_t(1) << 31)) return YOCOPP_EINVAL;  // tile row coordinates stay 32-bit
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return YOCOPP_ECUDA;
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < chunk_workspace_bytes(cache, sms))
+        return YOCOPP_EWORKSPACE;
+    if (total_q == 0 || max_q == 0) return YOCOPP_OK;
+
+    ChunkParams p = {};
+    p.q = static_cast<const uint8_t*>(q);
+    p.out = static_cast<uint8_t*>(out);
+    p.pos = pos;
+    p.cu_q = cu_q;
+    p.block_table = cache->block_table;
+    p.tree = reinterpret_cast<const unsigned long long*>(tree_mask);
+    p.total_q = total_q;
+    p.n_uniform = cu_q ? 0 : n_uniform;
+    p.max_q = max_q;
+    p.window = window;
+    p.batch = cache->batch;
+    p.hq = num_q_heads;
+    p.hkv = cache->num_kv_heads;
+    p.G = G;
+    p.capacity = cache->capacity;
+    p.block_size = paged ? cache->block_size : 0;
+    p.mbps = paged ? cache->max_blocks_per_seq : 0;
+    p.num_blocks = paged ? cache->num_blocks : 0;
+    const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(float(cache->head_dim));
+    p.qscale = sc * 1.4426950408889634f;
+    p.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+    p.drop_tile = g_test_drop_tile.load(std::memory_order_relaxed);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cache->head_dim == 128 ? launch_chunk_any<128>(cache, p, rows, max_q * G, sms, workspace, st)
+                                  : launch_chunk_any<64>(cache, p, rows, max_q * G, sms, workspace, st);
+}
+
+int32_t yocopp_rope_compose_append(const void* K1, const void* V1, const void* Ki, const void* Vi,
+                                   const float alpha[4], float lambda, const yocopp_rope* rope,
+                                   const int32_t* positions, const yocopp_cache* cache, const int32_t* pos,
+                                   const void* q, void* q_out, int32_t num_q_heads, const int32_t* cu_new,
+                                   int32_t n_uniform, int64_t total_new, void* stream) {
+    const int32_t rc = check_cache(cache);
+    if (rc != YOCOPP_OK) return rc;
+    if (rope == nullptr || positions == nullptr || total_new < 0 || total_new > (int64_t(1) << 31) - 1) return YOCOPP_EINVAL;
+    if (rope->rotary_dim < 2 || rope->rotary_dim % 2 != 0 || rope->rotary_dim > cache->head_dim) return YOCOPP_EINVAL;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return YOCOPP_EINVAL;
+    if (rope->num_axes < 1 || rope->num_axes > YOCOPP_ROPE_MAX_AXES) return YOCOPP_EINVAL;
+    const int pairs = rope->rotary_dim / 2;
+    for (int i = 0; i < pairs; ++i)
+        if (rope->axis[i] < 0 || rope->axis[i] >= rope->num_axes || !std::isfinite(rope->inv_freq[i])) return YOCOPP_EINVAL;
+    const bool any = K1 != nullptr || V1 != nullptr || Ki != nullptr || Vi != nullptr;
+    if (any) {
+        if (alpha == nullptr || pos == nullptr) return YOCOPP_EINVAL;
+        if (!std::isfinite(lambda) || !std::isfinite(alpha[0]) || !std::isfinite(alpha[1]) ||
+            !std::isfinite(alpha[2]) || !std::isfinite(alpha[3]))
+            return YOCOPP_EINVAL;
+        if (K1 == nullptr || V1 == nullptr || Ki == nullptr || Vi == nullptr) return YOCOPP_EINVAL;
+        if (!aligned(K1, 16) || !aligned(V1, 16) || !aligned(Ki, 16) || !aligned(Vi, 16)) return YOCOPP_EINVAL;
+        if (cu_new == nullptr && (n_uniform < 0 || int64_t(n_uniform) * cache->batch != total_new)) return YOCOPP_EINVAL;
+    }
+    if ((q == nullptr) != (q_out == nullptr)) return YOCOPP_EINVAL;
+    if (!any && q == nullptr && total_new > 0) return YOCOPP_EINVAL;  // nothing to turn
+    if (q != nullptr && (num_q_heads < 1 || !aligned(q, 16) || !aligned(q_out, 16))) return YOCOPP_EINVAL;
+    if (total_new == 0) return YOCOPP_OK;
+    const int sms = sm_count(current_device());
+    if (sms <= 0) return YOCOPP_ECUDA;
+
+    RopeParams p = {};
+    p.c.k1 = static_cast<const uint8_t*>(K1);
+    p.c.v1 = static_cast<const uint8_t*>(V1);
+    p.c.ki = static_cast<const uint8_t*>(Ki);
+    p.c.vi = static_cast<const uint8_t*>(Vi);
+    p.c.ck = static_cast<uint8_t*>(cache->k);
+    p.c.cv = static_cast<uint8_t*>(cache->v);
+    p.c.block_table = cache->block_table;
+    p.c.pos = pos;
+    p.c.cu_new = cu_new;
+    if (any) {
+        p.c.ak1 = alpha[0];
+        p.c.ak2 = alpha[1];
+        p.c.av1 = alpha[2];
+        p.c.av2 = alpha[3];
+        p.c.lam = lambda;
+    }
+    p.c.hkv = cache->num_kv_heads;
+    p.c.batch = cache->batch;
+    p.c.n_uniform = n_uniform;
+    p.c.capacity = cache->capacity;
+    p.c.block_size = cache->block_table ? cache->block_size : 0;
+    p.c.mbps = cache->block_table ? cache->max_blocks_per_seq : 0;
+    p.c.num_blocks = cache->block_table ? cache->num_blocks : 0;
+    p.c.bs_log2 = cache->block_table ? ilog2(cache->block_size) : 0;
+    p.q = static_cast<const uint8_t*>(q);
+    p.qo = static_cast<uint8_t*>(q_out);
+    p.positions = positions;
+    p.total = total_new;
+    p.hq = q != nullptr ? num_q_heads : 0;
+    p.pairs = pairs;
+    for (int i = 0; i < pairs; ++i) {
+        p.turns[i] = rope->inv_freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+        p.axis[i] = uint8_t(rope->axis[i]);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool il = rope->interleaved != 0;
+    if (cache->dtype == YOCOPP_BF16)
+        return cache->head_dim == 128 ? launch_rope<__nv_bfloat16, 128>(p, il, sms, st)
+                                      : launch_rope<__nv_bfloat16, 64>(p, il, sms, st);
+    return cache->head_dim == 128 ? launch_rope<float, 128>(p, il, sms, st) : launch_rope<float, 64>(p, il, sms, st);
+}
+
+int64_t yocopp_pages_workspace_size(const yocopp_cache* caches, int32_t num_caches) {
+    const int32_t rc = check_pages(caches, num_caches);
+    if (rc != YOCOPP_OK) return rc;
+    return int64_t(pages_layout(size_t(caches->num_blocks), size_t(caches->batch)).bytes);
+}
+
+int32_t yocopp_pages_resize(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, const int32_t* seqs,
+                            const int32_t* lens, int32_t n, int32_t* held, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+    const int32_t rc = check_pages(caches, num_caches);
+    if (rc != YOCOPP_OK) return rc;
+    if (block_refs == nullptr || n < 0 || n > caches->batch) return YOCOPP_EINVAL;
+    if (n == 0) return YOCOPP_OK;
+    if (seqs == nullptr || lens == nullptr || held == nullptr) return YOCOPP_EINVAL;
+    PagesParams p = {};
+    p.refs = block_refs;
+    p.a = seqs;
+    p.lens = lens;
+    p.held = held;
+    p.n = n;
+    return launch_pages<kPagesResize>(caches, num_caches, p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int32_t yocopp_pages_fork(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, const int32_t* src,
+                          const int32_t* dst, const int32_t* lens, int32_t n, int32_t deep, int32_t* held,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+    const int32_t rc = check_pages(caches, num_caches);
+    if (rc != YOCOPP_OK) return rc;
+    if (block_refs == nullptr || n < 0 || n > caches->batch || (deep != 0 && deep != 1)) return YOCOPP_EINVAL;
+    if (n == 0) return YOCOPP_OK;
+    if (src == nullptr || dst == nullptr || lens == nullptr || held == nullptr) return YOCOPP_EINVAL;
+    PagesParams p = {};
+    p.refs = block_refs;
+    p.a = src;
+    p.b = dst;
+    p.lens = lens;
+    p.held = held;
+    p.n = n;
+    p.deep = deep;
+    return launch_pages<kPagesFork>(caches, num_caches, p, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int32_t yocopp_pages_compact(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, int32_t* live,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+    const int32_t rc = check_pages(caches, num_caches);
+    if (rc != YOCOPP_OK) return rc;
+    if (block_refs == nullptr || live == nullptr) return YOCOPP_EINVAL;
+    PagesParams p = {};
+    p.refs = block_refs;
+    p.held = live;
+    return launch_pages<kPagesCompact>(caches, num_caches, p, workspace, workspace_bytes,
+                                       static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -337,6 +337,178 @@ int32_t yocopp_prefill_compose_attn(const void* K1, const void* V1, const void* 
                                     int64_t workspace_bytes, void* stream);
 
 /*
+ * yocopp_chunk_attn - attention of a chunk of new tokens over a cache: the
+ * next tokens of a long prompt, several tokens of a conversation at once, or
+ * the drafts of speculative decoding, over what is cached already (You Only
+ * Cache Once, abstract: a self-decoder's efficient attention, here a sliding
+ * window, and the cross-decoder's attention over the shared cache).  Every
+ * type, head size and cache layout of yocopp_cache; call it after the chunk's
+ * own rows are appended.
+ *
+ * Query row j of sequence b sits at cache position p_b + j (p_b = pos[b], or 0
+ * when pos == NULL).  For query head h and KV head g = h / (num_q_heads /
+ * num_kv_heads), over the positions u that the row sees:
+ *   s_u = scale * <q[b,j,h,:], K'[b,g,u,:]>,
+ *   out[b,j,h,:] = sum_u softmax(s)_u * V'[b,g,u,:].
+ * The row sees
+ *   causal (window == 0, tree_mask == NULL) : u in [0, p_b + j];
+ *   window > 0                              : u in (p_b + j - window, p_b + j];
+ *   tree_mask != NULL                       : u in [0, p_b), and p_b + c for
+ *     every set bit c < n_b of the row's word (a node of a token tree sets its
+ *     own bit and its ancestors').  At most 64 rows per sequence; excludes a
+ *     window.
+ * A row that sees nothing (pos 0 and an empty word) gives zeros.  What lies at
+ * positions a row does not see never reaches its output, NaN and infinities
+ * included; a score of +inf or NaN makes its whole row NaN.  Positions that no
+ * row of a row tile sees are not read, block by block, so a sequence's blocks
+ * below every window may have been released (entries -1), at 256 positions'
+ * grain: blocks that hold no position from (first window's start rounded down
+ * to 128) on.
+ * Scores, softmax statistics and sums are fp32; with bf16 the probabilities are
+ * rounded to bf16 for the value product (2^-9 relative each at most, shared by
+ * the row sum).
+ *
+ * The (row tile, key tile) pairs of all sequences are dealt out to the GPU's
+ * SMs in equal shares, so a single long sequence uses all of them; a second
+ * launch merges the row tiles that were split.  Results do not depend on
+ * timing.
+ *
+ *   q         : device [total_q][num_q_heads][head_dim], cache dtype, 16-byte
+ *               aligned, packed over the batch as for yocopp_prefill_attn.
+ *   pos, cu_q, n_uniform, total_q : as for yocopp_prefill_attn.
+ *   max_q     : with cu_q, an upper bound of every n_b; it chooses the kernel's
+ *               row tile; ignored when cu_q == NULL.
+ *   tree_mask : device uint64 [total_q], 8-byte aligned, or NULL.
+ *   window    : positions a row sees at most, itself included; 0 = all.
+ *   out       : device, like q; may not overlap it.
+ *   num_q_heads : any multiple of num_kv_heads.
+ *   scale     : softmax scale; 0 selects 1/sqrt(head_dim).
+ *   workspace : device, >= yocopp_chunk_attn_workspace_size() bytes, 256-byte
+ *               aligned, not shared with a concurrently running call.  It needs
+ *               no clearing and carries nothing from call to call.
+ * A sequence with p_b < 0, p_b + n_b > capacity or n_b > max_q is skipped and
+ * YOCOPP_ECAPACITY recorded on the device; a cu_q that decreases or leaves
+ * [0, total_q] skips the sequence with YOCOPP_EDEVICE_CHECK.  A block-table
+ * entry outside [0, num_blocks) records YOCOPP_EDEVICE_CHECK; the block is not
+ * read and the rows that see it are undefined.  Output rows of skipped
+ * sequences are not written.
+ */
+int64_t yocopp_chunk_attn_workspace_size(const yocopp_cache* cache, int32_t num_q_heads);
+int32_t yocopp_chunk_attn(const void* q, const yocopp_cache* cache, const int32_t* pos, const int32_t* cu_q,
+                          int32_t n_uniform, int64_t total_q, int32_t max_q, const uint64_t* tree_mask,
+                          int32_t window, void* out, int32_t num_q_heads, float scale, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions with one to four axes (time, height, width, ...).  The
+ * first rotary_dim channels of a head form rotary_dim / 2 pairs: channels
+ * (2c, 2c + 1) when interleaved, else (c, c + rotary_dim / 2).  Pair c belongs
+ * to axis axis[c] and turns by the angle position * inv_freq[c] of that axis;
+ * the channels from rotary_dim on pass unturned.
+ */
+#define YOCOPP_ROPE_MAX_AXES 4
+#define YOCOPP_ROPE_MAX_PAIRS 64
+typedef struct yocopp_rope {
+    int32_t rotary_dim;   /* even, 2 .. head_dim */
+    int32_t interleaved;  /* 0 or 1 */
+    int32_t num_axes;     /* 1 .. YOCOPP_ROPE_MAX_AXES */
+    int32_t reserved;
+    int32_t axis[YOCOPP_ROPE_MAX_PAIRS];
+    double inv_freq[YOCOPP_ROPE_MAX_PAIRS];  /* radians per position */
+} yocopp_rope;
+
+/*
+ * yocopp_rope_compose_append - yocopp_compose_append with rotary positions, and
+ * the chunk's queries turned in the same launch.  Let R_t turn the pairs of a
+ * head by token t's angles: (x, y) -> (x cos - y sin, y cos + x sin).  Then
+ *   K'[t,h,:]  = R_t lambda (alpha[0] K1[t,h,:] + alpha[1] Ki[t,h,:])
+ *   V'[t,h,:]  = lambda (alpha[2] V1[t,h,:] + alpha[3] Vi[t,h,:])
+ *   q_out[t,h,:] = R_t q[t,h,:]
+ * K1 and Ki are given unturned (R_t is linear: turning the composition equals
+ * composing turned keys).  V' has the bits of yocopp_compose_append.  K' is
+ * composed and turned in fp32 and rounded once.  Angles are reduced to a
+ * fraction of a turn in fp64, so every int32 position keeps full accuracy.
+ *
+ *   K1, V1, Ki, Vi, alpha, lambda, pos, cu_new, n_uniform, total_new : as for
+ *               yocopp_compose_append.  K1 = V1 = Ki = Vi = NULL turns queries
+ *               only (a cross-decoder layer, which appends nothing); the cache
+ *               then gives the type and head size, and alpha, pos and cu_new
+ *               are ignored.
+ *   rope      : HOST descriptor, read during the call.
+ *   positions : device int32 [num_axes][total_new], any value.
+ *   q, q_out  : device [total_new][num_q_heads][head_dim], 16-byte aligned, the
+ *               same tensor or not overlapping; both NULL: no queries.
+ * total_new < 2^31.  A row with no place in the cache is skipped and recorded
+ * as by yocopp_compose_append; its query is turned all the same.
+ */
+int32_t yocopp_rope_compose_append(const void* K1, const void* V1, const void* Ki, const void* Vi,
+                                   const float alpha[4], float lambda, const yocopp_rope* rope,
+                                   const int32_t* positions, const yocopp_cache* cache, const int32_t* pos,
+                                   const void* q, void* q_out, int32_t num_q_heads, const int32_t* cu_new,
+                                   int32_t n_uniform, int64_t total_new, void* stream);
+
+/*
+ * Pages of the paged caches, given and taken back on the device.  The layers
+ * of a model share one block table (the same positions lie in the same blocks
+ * of every layer's pool), so these calls take all layers' caches at once:
+ * num_caches (1 .. 128) descriptors, HOST array, alike in all but k and v.
+ * They WRITE the block table and the pools.
+ *
+ *   block_refs : device int32 [num_blocks], how many table entries name the
+ *                block; 0 = free.  Zero-filled for an empty pool.
+ * A row of the table holds blocks in its leading entries; every other entry is
+ * negative (fill the table with -1 for an empty pool).  Free blocks are given
+ * out in ascending order of their number, to the requests in order.  When the
+ * blocks run out, that request and every later one that needs any is refused:
+ * its row keeps what it held, its held is -1 and YOCOPP_ECAPACITY is recorded.
+ * A request that names a row outside [0, batch), or a row that an earlier
+ * request names, is refused with YOCOPP_EDEVICE_CHECK; one whose length is
+ * negative or above capacity, with YOCOPP_ECAPACITY.
+ *   workspace  : device, >= yocopp_pages_workspace_size() bytes, 256-byte
+ *                aligned, not shared with a concurrently running call; it needs
+ *                no clearing and carries nothing from call to call.
+ * Each call is two launches: the table, then the copies.
+ *
+ * yocopp_pages_resize - row seqs[i] is to hold lens[i] tokens (n requests,
+ * device int32 [n] each, n <= batch; a row not named is left as it is).
+ * Growing adds blocks; shrinking takes the blocks past the end back (free once
+ * no row names them); 0 ends a sequence.  All blocks of shrinking rows are
+ * taken back before any is given out.  Copy on write: where a row does not grow
+ * and its last block is kept in part (lens[i] is no multiple of block_size)
+ * and is still named by another row, the row gets a block of its own with that
+ * block's lens[i] mod block_size rows, so the tokens appended next land in no
+ * other sequence.  (A row that grows appends past its end; call resize with its
+ * present length first if its last block is shared.)  If no block is left for
+ * the copy the request is refused after the blocks past the end were taken
+ * back.
+ *   held : device int32 [n], blocks the row holds afterwards, or -1.
+ *
+ * yocopp_pages_fork - row dst[i], which has to be empty, gets the first lens[i]
+ * tokens of row src[i].  deep == 0: full blocks are shared and a last block
+ * that is held in part is copied; deep == 1: every block is copied.  lens[i]
+ * above what the source holds is refused with YOCOPP_ECAPACITY, a dst that is
+ * not empty or equals src with YOCOPP_EDEVICE_CHECK.  A source may be named by
+ * several requests.  A row that one request names as dst counts as empty for
+ * those that name it as src.
+ *   held : device int32 [n], blocks of the new row, or -1.
+ *
+ * yocopp_pages_compact - moves the blocks with references into the first
+ * *live places of the pools (the k-th such block past the end into the k-th
+ * hole), and rewrites the table and block_refs; afterwards a pool can be cut to
+ * *live blocks.
+ *   live : device int32 [1], blocks with references.
+ */
+int64_t yocopp_pages_workspace_size(const yocopp_cache* caches, int32_t num_caches);
+int32_t yocopp_pages_resize(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, const int32_t* seqs,
+                            const int32_t* lens, int32_t n, int32_t* held, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+int32_t yocopp_pages_fork(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, const int32_t* src,
+                          const int32_t* dst, const int32_t* lens, int32_t n, int32_t deep, int32_t* held,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+int32_t yocopp_pages_compact(const yocopp_cache* caches, int32_t num_caches, int32_t* block_refs, int32_t* live,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * yocopp_get_device_status - the first error code recorded by a kernel on
  * the current device since the last reset (YOCOPP_OK if none).  Synchronous:
  * it waits for the device.  reset != 0 clears the record.
