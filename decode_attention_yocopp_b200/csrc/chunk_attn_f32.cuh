@@ -38,7 +38,7 @@ struct ChunkF32 {
     static constexpr int P_OFF = Q_OFF + ROWS * QS * 4;
     static constexpr int ML_OFF = P_OFF + ROWS * PS * 4;
     static constexpr int BAR_OFF = ML_OFF + 2 * ROWS * 4;
-    static constexpr int SMEM = 1024 + BAR_OFF + (2 * STAGES + 1) * 8;
+    static constexpr int SMEM = 1024 + BAR_OFF + 2 * STAGES * 8;
     static constexpr int CTAS_PER_SM = D == 64 ? 2 : 1;
     static constexpr int THREADS = 288;  // 8 computing warps and the loader
 };
@@ -54,8 +54,6 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __shared__ int64_t s_scan[S::THREADS / 32];
     __shared__ ChunkStart s_start;
 
-    griddep_launch_dependents();
-    griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -65,16 +63,20 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     float* s_l = s_m + S::ROWS;
     uint64_t* full = reinterpret_cast<uint64_t*>(base + S::BAR_OFF);
     uint64_t* empty = full + S::STAGES;
-    uint64_t* merge_bar = empty + S::STAGES;
     if (tid == 0) {
         for (int s = 0; s < S::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 8);
         }
-        mbar_init(merge_bar, 8);
         fence_mbar_init();
         s_abort = 0;
     }
+    if (warp == 8 && lane == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    griddep_launch_dependents();
+    griddep_wait();
     chunk_find_start<RT, TK>(p, cta, s_scan, &s_start);
     if (s_start.item >= s_start.end) {
         if (tid == 0) __stcg(&p.desc[cta].last_cta, -1);
@@ -85,61 +87,39 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 
     if (warp == 8) {
         // ------------------------------------------------------------------ loader
-        if (lane == 0) {
-            const int nsb = TK / p.boxr;
-            int issued = 0;
-            bool ok = true;
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-            while (ok && walk.next(g)) {
-                const int plane_row = (g.b * p.hkv + g.g) * p.capacity;
-                for (int t = g.t0; t < g.t1; ++t) {
-                    const int slot = issued % S::STAGES;
-                    int rows[TK / 16], nb = 0;
+        int issued = 0;
+        bool ok = true;
+        while (ok && walk.next(g)) {
+            for (int t = g.t0; t < g.t1; ++t) {
+                const int slot = issued % S::STAGES;
+                const int crow = chunk_box_row<TK>(p, g, t, lane);
+                const unsigned boxes = __ballot_sync(0xffffffffu, crow >= 0);
+                if (lane == 0) ok = !s_abort && mbar_wait(&empty[slot], ((issued / S::STAGES) & 1) ^ 1, p.wait_limit_ns);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (!(cta == 0 && g.item + (t - g.t0) == p.drop_tile)) {  // failure injection (tests)
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[slot], uint32_t(2 * __popc(boxes) * p.boxr * 128 * S::NBOX));
+                    __syncwarp();
+                    if (crow >= 0) {
+                        uint8_t* dst = base + slot * S::STAGE_BYTES + lane * p.boxr * 128;
 #pragma unroll
-                    for (int sb = 0; sb < TK / 16; ++sb) {
-                        rows[sb] = -1;
-                        const int at = t * TK + sb * p.boxr;
-                        if (sb < nsb && at <= g.span.hi && at + p.boxr > g.span.lo) {
-                            if (p.block_table == nullptr) {
-                                rows[sb] = plane_row + at;
-                            } else {
-                                const int blk = __ldg(p.block_table + int64_t(g.b) * p.mbps + at / p.block_size);
-                                if (blk < 0 || blk >= p.num_blocks)
-                                    record_status(YOCOPP_EDEVICE_CHECK);
-                                else
-                                    rows[sb] = (blk * p.hkv + g.g) * p.block_size + at % p.block_size;
-                            }
-                            nb += rows[sb] >= 0;
-                        }
-                    }
-                    if (s_abort || !mbar_wait(&empty[slot], ((issued / S::STAGES) & 1) ^ 1, p.wait_limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const bool drop = cta == 0 && g.item + (t - g.t0) == p.drop_tile;  // failure injection (tests)
-                    if (!drop) mbar_arrive_expect_tx(&full[slot], uint32_t(2 * nb * p.boxr * 128 * S::NBOX));
-                    uint8_t* dst = base + slot * S::STAGE_BYTES;
-#pragma unroll
-                    for (int sb = 0; sb < TK / 16; ++sb) {
-                        if (rows[sb] < 0 || drop) continue;
                         for (int bx = 0; bx < S::NBOX; ++bx) {
-                            tma_load_2d(dst + bx * S::BOXB + sb * p.boxr * 128, &tmK, &full[slot], bx * 32, rows[sb]);
-                            tma_load_2d(dst + S::TILE_BYTES + bx * S::BOXB + sb * p.boxr * 128, &tmV, &full[slot],
-                                        bx * 32, rows[sb]);
+                            tma_load_2d(dst + bx * S::BOXB, &tmK, &full[slot], bx * 32, crow);
+                            tma_load_2d(dst + S::TILE_BYTES + bx * S::BOXB, &tmV, &full[slot], bx * 32, crow);
                         }
                     }
-                    ++issued;
                 }
+                ++issued;
             }
-            if (!ok) {
-                record_status(YOCOPP_ETIMEOUT);
-                s_abort = 1;
-            }
-            if (!ok || s_abort)  // the copies in flight land before the CTA can exit
-                for (int t = max(0, issued - S::STAGES); t < issued; ++t)
-                    (void)mbar_wait(&full[t % S::STAGES], (t / S::STAGES) & 1, p.wait_limit_ns);
         }
+        if (!ok) {
+            record_status(YOCOPP_ETIMEOUT);
+            s_abort = 1;
+        }
+        if (!ok || s_abort)  // the copies in flight land before the CTA can exit
+            for (int t = max(0, issued - S::STAGES); t < issued; ++t)
+                (void)mbar_wait(&full[t % S::STAGES], (t / S::STAGES) & 1, p.wait_limit_ns);
         return;
     }
 
@@ -148,22 +128,20 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const int copy = C == 1 ? 0 : ty / (16 / C);
     const int lr0 = 4 * ty;                  // first of this thread's rows of the 64
     const int row0 = lr0 % RT;               // the same in the row tile
-    int tiles = 0, merges = 0;
+    int tiles = 0;
     bool ok = true, split_end = false;
-    auto meet = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(merge_bar);
-        return bool(__all_sync(0xffffffffu, mbar_wait(merge_bar, merges++ & 1, p.wait_limit_ns)));
-    };
+    // all computing warps come to every one of these, whatever happens: a wait that has run out (ok = false)
+    // changes no branch around them
+    auto meet = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     while (walk.next(g)) {
-        const int64_t rows_all = int64_t(g.s.n) * p.G;
+        const int rows_all = g.s.n * p.G;
         if (g.t0 == g.u0 && g.t1 < g.u1) {
             split_end = true;
             if (tid == 0) {
                 ChunkDesc* d = p.desc + cta;
                 __stcg(&d->row0, g.s.row0);
                 __stcg(&d->first_row, g.rt * RT);
-                __stcg(&d->rows, int(min(int64_t(RT), rows_all - int64_t(g.rt) * RT)));
+                __stcg(&d->rows, min(RT, rows_all - g.rt * RT));
                 __stcg(&d->g, g.g);
                 __stcg(&d->last_cta, chunk_cta_of(s_start.total, g.item + (g.u1 - g.u0) - 1, p.num_ctas));
             }
@@ -177,7 +155,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 const int R = g.rt * RT + lr % RT;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (R < rows_all) {
-                    const int j = R / p.G;
+                    const int j = chunk_token(p, R);
                     v = ld_stream(p.q + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) * (D * 4) + ch * 16);
                 }
                 *reinterpret_cast<uint4*>(sQ + lr * S::QS + ch * 4) = v;
@@ -187,9 +165,9 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         ChunkSight see[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            see[i] = chunk_sight(p, g.s, int(min(int64_t(g.rt * RT + row0 + i) / p.G, int64_t(g.s.n - 1))));
-        const int j0 = int(int64_t(g.rt) * RT / p.G);
-        const int j1 = int(min((int64_t(g.rt) * RT + RT - 1) / p.G, int64_t(g.s.n - 1)));
+            see[i] = chunk_sight(p, g.s, min(chunk_token(p, g.rt * RT + row0 + i), g.s.n - 1));
+        const int j0 = chunk_token(p, g.rt * RT);
+        const int j1 = min(chunk_token(p, g.rt * RT + RT - 1), g.s.n - 1);
         const int hi_all = p.tree ? g.s.p0 - 1 : g.s.p0 + j0;
         const int lo_all = !p.tree && p.window ? max(0, g.s.p0 + j1 + 1 - p.window) : 0;
         float m[4], l[4];
@@ -203,8 +181,9 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         for (int t = g.t0; t < g.t1; ++t) {
             const int slot = tiles % S::STAGES;
-            ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(&full[slot], (tiles / S::STAGES) & 1, p.wait_limit_ns));
-            if (!ok) break;
+            if (ok) ok = !s_abort && mbar_wait(&full[slot], (tiles / S::STAGES) & 1, p.wait_limit_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) s_abort = 1;
             ++tiles;
             const uint8_t* sK = base + slot * S::STAGE_BYTES;
             const uint8_t* sV = sK + S::TILE_BYTES;
@@ -309,7 +288,6 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < 2 * CPT; ++k) o[i][k] = ffma2(o[i][k], make_float2(corr[i], corr[i]), w[i][k]);
         }
-        if (!ok) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -322,7 +300,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             const int R = g.rt * RT + row;
             if (R >= rows_all) return;
             if (whole) {
-                const int j = R / p.G;
+                const int j = chunk_token(p, R);
                 *reinterpret_cast<float4*>(p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) *
                                                        int64_t(D * 4) + ch * 16) = v;
             } else {
@@ -353,8 +331,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     s_l[lr0 + i] = l[i];
                 }
             }
-            ok = meet();  // also: no warp reads its queries any more
-            if (!ok) break;
+            meet();  // also: no warp reads its queries any more
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float M = NEG_INF_F, L = 0.f;
@@ -375,8 +352,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     *reinterpret_cast<float4*>(sQ + (lr0 + i) * S::QS + (tx + 16 * c) * 4) =
                         make_float4(o[i][2 * c].x * w, o[i][2 * c].y * w, o[i][2 * c + 1].x * w, o[i][2 * c + 1].y * w);
             }
-            ok = meet();
-            if (!ok) break;
+            meet();
             for (int i = tid; i < RT * (D / 4); i += 256) {
                 const int row = i / (D / 4), ch = i % (D / 4);
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -390,14 +366,10 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 }
                 put(row, ch, s);
             }
-            ok = meet();
-            if (!ok) break;
+            meet();
         }
     }
-    if (!ok) {
-        record_status(YOCOPP_ETIMEOUT);
-        s_abort = 1;
-    }
+    if (!ok) record_status(YOCOPP_ETIMEOUT);
     if (tid == 0 && !split_end) __stcg(&p.desc[cta].last_cta, -1);
 }
 

@@ -29,8 +29,8 @@
 // tile's span are zeroed in shared memory, and where another value is not
 // finite it is zeroed too and added, by hand, to the rows that see its key.
 //
-// Warps: 0 = TMA producer (lane 0: K, lane 1: V), 1 = MMA issuer and tensor-
-// memory owner, 2..5 = half 0, 6..9 = half 1 (they also load the queries).
+// Warps: 0 = K loader, 10 = V loader, 1 = MMA issuer and tensor-memory owner,
+// 2..5 = half 0, 6..9 = half 1 (they also load the queries).
 // Rings and barriers run on across the segments of a CTA: the producer is
 // already loading the next segment's tiles, and the next queries are in place,
 // while a segment's result is written.  Every wait is bounded; on a timeout
@@ -58,10 +58,10 @@ struct ChunkTc {
     static constexpr int K_OFF = SCR_OFF + SCR_BYTES;
     static constexpr int V_OFF = K_OFF + KSLOTS * TILE_BYTES;
     static constexpr int BAR_OFF = V_OFF + VSLOTS * TILE_BYTES;
-    // q_full[2], k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], o_last[2], scan[2], merge, drain
-    static constexpr int NBAR = 2 + 2 * KSLOTS + 2 * VSLOTS + 10;
+    // q_full[2], k_full, k_empty, v_full, v_empty, s_full[2], p_full[2], o_last[2], drain
+    static constexpr int NBAR = 2 + 2 * KSLOTS + 2 * VSLOTS + 7;
     static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = 352;
     static constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, XK, false);
     static constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, true);
     // tensor memory: S_x at 128 x (PAIR: P_x over its first 64 columns; else P_x at 128 x + 64), O_x at 256 + 128 x
@@ -111,8 +111,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     __shared__ int64_t s_scan[S::THREADS / 32];
     __shared__ ChunkStart s_start;
 
-    griddep_launch_dependents();  // the merge's blocks take their places beside these CTAs and wait for their end
-    griddep_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -124,9 +122,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     uint64_t* s_full = v_empty + S::VSLOTS;  // [2]
     uint64_t* p_full = s_full + 2;           // [2]
     uint64_t* o_last = p_full + 2;           // [2]
-    uint64_t* scan_bar = o_last + 2;         // [0] both halves, [1] half 0 alone
-    uint64_t* merge_bar = scan_bar + 2;
-    uint64_t* drain = merge_bar + 1;
+    uint64_t* drain = o_last + 2;
 
     if (tid == 0) {
         for (int s = 0; s < S::KSLOTS; ++s) {
@@ -143,100 +139,78 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             mbar_init(&p_full[x], 4);
             mbar_init(&o_last[x], 1);
         }
-        mbar_init(&scan_bar[0], 8);
-        mbar_init(&scan_bar[1], 4);
-        mbar_init(merge_bar, 8);
         mbar_init(drain, 1);
         fence_mbar_init();
         s_abort = 0;
         s_cdone = 0;
         s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0u;
     }
-    chunk_find_start<RT, TK>(p, cta, s_scan, &s_start);
-    if (s_start.item >= s_start.end) {  // nothing for this CTA
-        if (tid == 0) __stcg(&p.desc[cta].last_cta, -1);
-        return;
-    }
+    // before the wait: nothing here depends on the previous kernel
+    if (warp == 0 && lane == 0) prefetch_tensormap(&tmK);
+    if (warp == 10 && lane == 0) prefetch_tensormap(&tmV);
     if (warp == 1) {
         tmem_alloc(&s_tmem, S::TMEM_COLS);
         tmem_relinquish();
     }
+    griddep_launch_dependents();  // the merge's blocks take their places beside these CTAs and wait for their end
+    griddep_wait();
     tc_fence_before();
-    __syncthreads();
+    chunk_find_start<RT, TK>(p, cta, s_scan, &s_start);  // ends with a block-wide barrier
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-
+    if (s_start.item >= s_start.end) {  // nothing for this CTA
+        if (tid == 0) __stcg(&p.desc[cta].last_cta, -1);
+        if (warp == 1) tmem_dealloc(tmem, S::TMEM_COLS);
+        return;
+    }
     ChunkWalk<RT, TK> walk(p, s_start);
     ChunkSegment sg;
     // does half 1 have rows in this segment
-    auto both = [&](const ChunkSegment& g) { return !PAIR || int64_t(g.s.n) * p.G > int64_t(g.rt) * RT + 128; };
+    auto both = [&](const ChunkSegment& g) { return !PAIR || g.s.n * p.G > g.rt * RT + 128; };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------------ producers
-        if (lane < 2) {
-            const bool kl = lane == 0;
-            const CUtensorMap* map = kl ? &tmK : &tmV;
-            uint64_t* full = kl ? k_full : v_full;
-            uint64_t* empty = kl ? k_empty : v_empty;
-            uint8_t* ring = base + (kl ? S::K_OFF : S::V_OFF);
-            const int slots = kl ? S::KSLOTS : S::VSLOTS;
-            const int nsb = TK / p.boxr;
-            int slot = 0, round = 0, issued = 0;
-            bool ok = true;
-            prefetch_tensormap(map);
-            while (ok && walk.next(sg)) {
-                const int plane_row = (sg.b * p.hkv + sg.g) * p.capacity;
-                for (int t = sg.t0; t < sg.t1; ++t) {
-                    // one box (contiguous) or one per cache block; a box that no row of the tile sees is not
-                    // loaded.  The table is read before the wait for the slot.
-                    int rows[TK / 16], nb = 0;
+    if (warp == 0 || warp == 10) {
+        // ------------------------------------------------------------------ loaders
+        const bool kl = warp == 0;
+        const CUtensorMap* map = kl ? &tmK : &tmV;
+        uint64_t* full = kl ? k_full : v_full;
+        uint64_t* empty = kl ? k_empty : v_empty;
+        uint8_t* ring = base + (kl ? S::K_OFF : S::V_OFF);
+        const int slots = kl ? S::KSLOTS : S::VSLOTS;
+        int slot = 0, round = 0, issued = 0;
+        bool ok = true;
+        while (ok && walk.next(sg)) {
+            for (int t = sg.t0; t < sg.t1; ++t) {
+                // the table is read before the wait for the slot
+                const int crow = chunk_box_row<TK>(p, sg, t, lane);
+                const unsigned boxes = __ballot_sync(0xffffffffu, crow >= 0);
+                if (lane == 0) ok = !s_abort && mbar_wait(&empty[slot], (round & 1) ^ 1, p.wait_limit_ns);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                if (!(kl && cta == 0 && sg.item + (t - sg.t0) == p.drop_tile)) {  // failure injection (tests)
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(boxes) * p.boxr * 128 * S::NBOX));
+                    __syncwarp();
+                    if (crow >= 0) {
 #pragma unroll
-                    for (int sb = 0; sb < TK / 16; ++sb) {
-                        rows[sb] = -1;
-                        const int at = t * TK + sb * p.boxr;
-                        if (sb < nsb && at <= sg.span.hi && at + p.boxr > sg.span.lo) {
-                            if (p.block_table == nullptr) {
-                                rows[sb] = plane_row + at;
-                            } else {
-                                const int blk = __ldg(p.block_table + int64_t(sg.b) * p.mbps + at / p.block_size);
-                                if (blk < 0 || blk >= p.num_blocks)
-                                    record_status(YOCOPP_EDEVICE_CHECK);
-                                else
-                                    rows[sb] = (blk * p.hkv + sg.g) * p.block_size + at % p.block_size;
-                            }
-                            nb += rows[sb] >= 0;
-                        }
-                    }
-                    if (s_abort || !mbar_wait(&empty[slot], (round & 1) ^ 1, p.wait_limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!(kl && cta == 0 && sg.item + (t - sg.t0) == p.drop_tile)) {  // failure injection (tests)
-                        mbar_arrive_expect_tx(&full[slot], uint32_t(nb * p.boxr * 128 * S::NBOX));
-#pragma unroll
-                        for (int sb = 0; sb < TK / 16; ++sb) {
-                            if (rows[sb] < 0) continue;
-#pragma unroll
-                            for (int bx = 0; bx < S::NBOX; ++bx)
-                                tma_load_2d(ring + slot * S::TILE_BYTES + bx * S::BOXB + sb * p.boxr * 128, map,
-                                            &full[slot], bx * 64, rows[sb]);
-                        }
-                    }
-                    ++issued;
-                    if (++slot == slots) {
-                        slot = 0;
-                        ++round;
+                        for (int bx = 0; bx < S::NBOX; ++bx)
+                            tma_load_2d(ring + slot * S::TILE_BYTES + bx * S::BOXB + lane * p.boxr * 128, map,
+                                        &full[slot], bx * 64, crow);
                     }
                 }
+                ++issued;
+                if (++slot == slots) {
+                    slot = 0;
+                    ++round;
+                }
             }
-            if (!ok) {
-                record_status(YOCOPP_ETIMEOUT);
-                s_abort = 1;
-            }
-            if (!ok || s_abort)  // the copies in flight land before the CTA can exit
-                for (int t = max(0, issued - slots); t < issued; ++t)
-                    (void)mbar_wait(&full[t % slots], (t / slots) & 1, p.wait_limit_ns);
         }
+        if (!ok) {
+            record_status(YOCOPP_ETIMEOUT);
+            s_abort = 1;
+        }
+        if (!ok || s_abort)  // the copies in flight land before the CTA can exit
+            for (int t = max(0, issued - slots); t < issued; ++t)
+                (void)mbar_wait(&full[t % slots], (t / slots) & 1, p.wait_limit_ns);
         return;
     }
 
@@ -360,7 +334,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!PAIR && x == 0) return;
         constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes
         const int ch = lane % CH;
-        const int64_t rows_all = int64_t(g.s.n) * p.G;
+        const int rows_all = g.s.n * p.G;
         uint4 v[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -368,7 +342,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const int R = g.rt * RT + (PAIR ? 128 * x + rr : rr % RT);
             v[i] = make_uint4(0u, 0u, 0u, 0u);
             if (R < rows_all) {
-                const int j = R / p.G;
+                const int j = chunk_token(p, R);
                 v[i] = ld_stream(p.q + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) * (D * 2) + ch * 16);
             }
         }
@@ -382,15 +356,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
     };
-    int merges = 0, scans = 0, scans_alone = 0;
-    // the warps that arrive on a barrier meet (bounded)
-    auto meet = [&](uint64_t* bar, int& count) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-        return bool(__all_sync(0xffffffffu, mbar_wait(bar, count++ & 1, p.wait_limit_ns)));
+    // The softmax warps' own barriers are named ones: all of them come to every one, whatever happens, as a
+    // wait that has run out (ok = false) changes no branch around a barrier; it only makes later waits be
+    // skipped.  Barrier 1: both halves, 2: half 0 alone.
+    auto meet = [&](bool two) {
+        if (two) asm volatile("bar.sync 1, 256;" ::: "memory");
+        else asm volatile("bar.sync 2, 128;" ::: "memory");
     };
-    auto meet_scan = [&](bool two) {
-        return two ? meet(&scan_bar[0], scans) : meet(&scan_bar[1], scans_alone);
+    bool ok = true;
+    auto await = [&](uint64_t* bar, int parity) {
+        if (ok) ok = !s_abort && mbar_wait(bar, parity, p.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) s_abort = 1;
     };
 
     if constexpr (!PAIR) {  // the columns of P that belong to other copies stay zero
@@ -401,7 +378,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     bool split_end = false;                          // this CTA leaves its last row tile unfinished
     int n_x = 0, n_seg = 0, vs = 0, vr = 0;
-    bool ok = true;
     bool have = walk.next(sg);
     if (have && (x == 0 || both(sg))) load_q(sg);
     while (have) {
@@ -415,21 +391,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 ChunkDesc* d = p.desc + cta;
                 __stcg(&d->row0, g.s.row0);
                 __stcg(&d->first_row, g.rt * RT);
-                __stcg(&d->rows, int(min(int64_t(RT), int64_t(g.s.n) * p.G - int64_t(g.rt) * RT)));
+                __stcg(&d->rows, min(RT, g.s.n * p.G - g.rt * RT));
                 __stcg(&d->g, g.g);
                 __stcg(&d->last_cta, chunk_cta_of(s_start.total, g.item + (g.u1 - g.u0) - 1, p.num_ctas));
             }
         }
         float m_ref = NEG_INF_F, l = 0.f;
         const int R = g.rt * RT + row;               // row of the sequence
-        const int64_t rows_all = int64_t(g.s.n) * p.G;
+        const int rows_all = g.s.n * p.G;
         if (mine) {
-            const int j = min(R / p.G, g.s.n - 1);
+            const int j = min(chunk_token(p, R), g.s.n - 1);
             ChunkSight see = chunk_sight(p, g.s, j);
             if (see.tree && g.s.n < 64) see.bits &= (1ull << g.s.n) - 1ull;
             // positions that every row of the row tile sees: [lo_all, hi_all]
-            const int j0 = int(int64_t(g.rt) * RT / p.G);
-            const int j1 = int(min((int64_t(g.rt) * RT + RT - 1) / p.G, int64_t(g.s.n - 1)));
+            const int j0 = chunk_token(p, g.rt * RT);
+            const int j1 = min(chunk_token(p, g.rt * RT + RT - 1), g.s.n - 1);
             const int hi_all = p.tree ? g.s.p0 - 1 : g.s.p0 + j0;
             const int lo_all = !p.tree && p.window ? max(0, g.s.p0 + j1 + 1 - p.window) : 0;
             {
@@ -440,8 +416,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 for (int c = 0; c < D / 32; ++c) tmem_st32(tO + uint32_t(c * 32), z);
             }
             for (int t = g.t0; t < g.t1; ++t) {
-                ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(&s_full[x], n_x & 1, p.wait_limit_ns));
-                if (!ok) break;
+                await(&s_full[x], n_x & 1);
                 ++n_x;
                 tc_fence_after();
                 const int key0 = t * TK;
@@ -519,8 +494,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
                 if (masked) {
                     // key row r of the value tile, this half's part of its chunks
-                    ok = __all_sync(0xffffffffu, mbar_wait(&v_full[vs], vr & 1, p.wait_limit_ns));
-                    if (!ok) break;
+                    await(&v_full[vs], vr & 1);
                     constexpr int CH = D / 8;
                     const int c0 = two && x == 1 ? CH / 2 : 0, c1 = two && x == 0 ? CH / 2 : CH;
                     uint8_t* vrow = base + S::V_OFF + vs * S::TILE_BYTES + r * 128;
@@ -537,8 +511,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         }
                     }
                     if (bad) atomicOr(&s_bad[r >> 5], 1u << (r & 31));
-                    ok = meet_scan(two);
-                    if (!ok) break;
+                    meet(two);
                     const volatile unsigned* vb = s_bad;
                     const unsigned any = vb[0] | vb[1] | vb[2] | vb[3];
                     if (any) {  // uniform over the CTA's softmax threads
@@ -560,8 +533,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                             __syncwarp();
                             tmem_st32(tO + uint32_t(c * 32), o);
                         }
-                        ok = meet_scan(two);
-                        if (!ok) break;
+                        meet(two);
                         if (bad) {
                             for (int ch = c0; ch < c1; ++ch) {
                                 uint16_t* a = reinterpret_cast<uint16_t*>(vrow + (ch >> 3) * S::BOXB +
@@ -583,7 +555,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-            if (!ok) break;
         } else {
             for (int t = 0; t < nt; ++t)
                 if (++vs == S::VSLOTS) {
@@ -596,8 +567,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!mine) continue;
 
         // ---- the segment's result: whole row tiles to the output, others to the workspace
-        ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(&o_last[x], n_seg & 1, p.wait_limit_ns));
-        if (!ok) break;
+        await(&o_last[x], n_seg & 1);
         ++n_seg;
         tc_fence_after();
         const bool whole = g.t0 == g.u0 && g.t1 == g.u1;
@@ -606,7 +576,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             const bool store = R < rows_all;
             const bool none = m_ref == NEG_INF_F;
             const float w = !whole ? 1.f : none ? 0.f : 1.f / l;
-            const int j = R / p.G;
+            const int j = chunk_token(p, R);
             uint8_t* orow = p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) * int64_t(D * 2);
             if (!whole && store) {
                 __stcg(slot + RT * D + row, m_ref);
@@ -641,8 +611,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             float* s_l = s_m + 256;
             s_m[me] = m_ref;
             s_l[me] = l;
-            ok = meet(merge_bar, merges);
-            if (!ok) break;
+            meet(true);
             float M = NEG_INF_F, L = 0.f;
 #pragma unroll
             for (int i = 0; i < NC; ++i) M = fmaxf(M, s_m[RT * i + row]);
@@ -651,8 +620,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const float mi = s_m[RT * i + row];
                 L += mi == NEG_INF_F ? 0.f : s_l[RT * i + row] * ex2_approx(mi - M);
             }
-            ok = meet(merge_bar, merges);  // read by all before it is written over
-            if (!ok) break;
+            meet(true);  // read by all before it is written over
             // a row that sees nothing gives zeros
             const float w = m_ref == NEG_INF_F ? 0.f : ex2_approx(m_ref - M) * (whole ? 1.f / L : 1.f);
             if (!whole && copy == 0 && x == 0 && R < rows_all) {
@@ -667,8 +635,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 for (int q4 = 0; q4 < 8; ++q4)
                     *reinterpret_cast<float4*>(scr + me * 128 + ((q4 ^ (me & 7)) << 4)) =
                         make_float4(o[q4 * 4] * w, o[q4 * 4 + 1] * w, o[q4 * 4 + 2] * w, o[q4 * 4 + 3] * w);
-                ok = meet(merge_bar, merges);
-                if (!ok) break;
+                meet(true);
 #pragma unroll
                 for (int i = 0; i < RT / 32; ++i) {
                     const int id = me + 256 * i, rr = id >> 3, q4 = id & 7;
@@ -685,7 +652,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     const int RR = g.rt * RT + rr;
                     if (RR >= rows_all) continue;
                     if (whole) {
-                        const int j = RR / p.G;
+                        const int j = chunk_token(p, RR);
                         uint2 v = make_uint2(float2_to_bf16x2(a.x, a.y), float2_to_bf16x2(a.z, a.w));
                         *reinterpret_cast<uint2*>(p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (RR - j * p.G)) *
                                                               int64_t(D * 2) + (c * 32 + q4 * 4) * 2) = v;
@@ -693,16 +660,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         __stcg(reinterpret_cast<float4*>(slot + int64_t(rr) * D + c * 32 + q4 * 4), a);
                     }
                 }
-                ok = meet(merge_bar, merges);
-                if (!ok) break;
+                meet(true);
             }
-            if (!ok) break;
         }
     }
-    if (!ok) {
-        record_status(YOCOPP_ETIMEOUT);
-        s_abort = 1;
-    }
+    if (!ok) record_status(YOCOPP_ETIMEOUT);
     if (warp == 2 && lane == 0 && !split_end) __stcg(&p.desc[cta].last_cta, -1);
     tc_fence_before();
     __syncwarp();

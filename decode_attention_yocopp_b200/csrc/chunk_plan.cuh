@@ -14,7 +14,7 @@
 // launch merges them.
 #pragma once
 
-#include "common.cuh"
+#include "compose_append.cuh"
 
 namespace yocopp {
 
@@ -30,7 +30,8 @@ struct ChunkParams {
     int64_t total_q;
     int32_t n_uniform, max_q, window;
     int32_t batch, hq, hkv, G, capacity;
-    int32_t block_size, mbps, num_blocks, boxr;
+    uint32_t g_m, g_s;           // division by G (fast_div); rows of a sequence are below 2^31
+    int32_t bs_log2, mbps, num_blocks, boxr;
     float qscale;                // softmax scale * log2(e)
     int32_t num_ctas;
     float* part;                 // [num_ctas][2][RT][D + 2]: o, then m, l
@@ -71,6 +72,9 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b, bool 
     return s;
 }
 
+// New token of row r.
+__device__ __forceinline__ int chunk_token(const ChunkParams& p, int r) { return int(fast_div(uint32_t(r), p.g_m, p.g_s)); }
+
 // Positions [lo, hi] that the rows of a row tile may see.
 struct ChunkSpan {
     int lo, hi;
@@ -82,7 +86,7 @@ __device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const Chun
         r.lo = 0;
         r.hi = s.p0 + s.n - 1;
     } else {
-        const int j0 = int(int64_t(rt) * RT / p.G), j1 = min(int((int64_t(rt) * RT + RT - 1) / p.G), s.n - 1);
+        const int j0 = chunk_token(p, rt * RT), j1 = min(chunk_token(p, rt * RT + RT - 1), s.n - 1);
         r.lo = p.window ? max(0, s.p0 + j0 + 1 - p.window) : 0;
         r.hi = s.p0 + j1;
     }
@@ -90,7 +94,7 @@ __device__ __forceinline__ ChunkSpan chunk_span(const ChunkParams& p, const Chun
 }
 template <int RT>
 __device__ __forceinline__ int chunk_row_tiles(const ChunkParams& p, const ChunkSeq& s) {
-    return int((int64_t(s.n) * p.G + RT - 1) / RT);
+    return (s.n * p.G + RT - 1) / RT;
 }
 template <int RT, int TK>
 __device__ __forceinline__ int64_t chunk_items_per_head(const ChunkParams& p, const ChunkSeq& s) {
@@ -117,14 +121,19 @@ struct ChunkStart {
     int64_t item, end, total;
 };
 
+// a / b of non-negative numbers, in 32 bits (a quarter of the time) where they fit
+__device__ __forceinline__ int64_t div_items(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 // first item of CTA c
 __device__ __forceinline__ int64_t chunk_first_item(int64_t total, int c, int num_ctas) {
-    return total / num_ctas * c + min(int64_t(c), total % num_ctas);
+    const int64_t q = div_items(total, num_ctas), r = total - q * num_ctas;
+    return q * c + min(int64_t(c), r);
 }
 // the CTA that has an item
 __device__ __forceinline__ int chunk_cta_of(int64_t total, int64_t item, int num_ctas) {
-    const int64_t q = total / num_ctas, r = total % num_ctas;
-    return int(item < r * (q + 1) ? item / (q + 1) : r + (item - r * (q + 1)) / q);
+    const int64_t q = div_items(total, num_ctas), r = total - q * num_ctas;
+    return int(item < r * (q + 1) ? div_items(item, q + 1) : r + div_items(item - r * (q + 1), q));
 }
 
 // All threads of the CTA call it; `start` is shared memory.  scan: one int64 per warp, shared.
@@ -163,7 +172,7 @@ __device__ __forceinline__ void chunk_find_start(const ChunkParams& p, int cta, 
                 at += per_head * p.hkv;
                 continue;
             }
-            const int g = int((w0 - at) / per_head);
+            const int g = int(div_items(w0 - at, per_head));
             int64_t rem = (w0 - at) - g * per_head;
             int rt = 0;
             for (;; ++rt) {
@@ -254,15 +263,20 @@ __device__ __forceinline__ ChunkSight chunk_sight(const ChunkParams& p, const Ch
     return r;
 }
 
-// Cache row of position u of (b, g), or -1 where its block is not valid (recorded).
-__device__ __forceinline__ int64_t chunk_cache_row(const ChunkParams& p, int b, int g, int u) {
-    if (p.block_table == nullptr) return (int64_t(b) * p.hkv + g) * p.capacity + u;
-    const int blk = __ldg(p.block_table + int64_t(b) * p.mbps + u / p.block_size);
+// The boxes of key tile t, one per lane: positions t TK + lane boxr .. + boxr - 1 (one box of a contiguous
+// cache's tile, one per block of a paged one).  Gives the first cache row, or -1 where the lane has no box,
+// no row of the row tile sees it, or its block is not valid (recorded).
+template <int TK>
+__device__ __forceinline__ int chunk_box_row(const ChunkParams& p, const ChunkSegment& sg, int t, int lane) {
+    const int at = t * TK + lane * p.boxr;
+    if (lane * p.boxr >= TK || at > sg.span.hi || at + p.boxr <= sg.span.lo) return -1;
+    if (p.block_table == nullptr) return (sg.b * p.hkv + sg.g) * p.capacity + at;
+    const int blk = __ldg(p.block_table + int64_t(sg.b) * p.mbps + (at >> p.bs_log2));
     if (blk < 0 || blk >= p.num_blocks) {
         record_status(YOCOPP_EDEVICE_CHECK);
         return -1;
     }
-    return (int64_t(blk) * p.hkv + g) * p.block_size + u % p.block_size;
+    return ((blk * p.hkv + sg.g) << p.bs_log2) + (at & ((1 << p.bs_log2) - 1));
 }
 
 // Slot of the workspace for a segment that is not a whole row tile: 0 where an earlier CTA began
@@ -312,8 +326,8 @@ __global__ void __launch_bounds__(kChunkMergeThreads) chunk_merge_kernel(const _
         }
     };
     auto store = [&](int r, float l, const float (&o)[C]) {
-        const int row = first_row + r;
-        const int64_t at = (int64_t(row0) + row / p.G) * p.hq + g * p.G + row % p.G;
+        const int row = first_row + r, j = chunk_token(p, row);
+        const int64_t at = (int64_t(row0) + j) * p.hq + g * p.G + (row - j * p.G);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int k = 0; k < C; ++k)

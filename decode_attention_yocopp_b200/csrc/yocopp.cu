@@ -1041,8 +1041,11 @@ int32_t yocopp_chunk_attn(const void* q, const yocopp_cache* cache, const int32_
     p.hq = num_q_heads;
     p.hkv = cache->num_kv_heads;
     p.G = G;
+    const FastDiv dg = make_fast_div(uint32_t(G));
+    p.g_m = dg.m;
+    p.g_s = dg.s;
     p.capacity = cache->capacity;
-    p.block_size = paged ? cache->block_size : 0;
+    p.bs_log2 = paged ? ilog2(cache->block_size) : 0;
     p.mbps = paged ? cache->max_blocks_per_seq : 0;
     p.num_blocks = paged ? cache->num_blocks : 0;
     const float sc = scale > 0.f ? scale : 1.0f / std::sqrt(float(cache->head_dim));
