@@ -54,7 +54,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __shared__ int64_t s_scan[S::THREADS / 32];
     __shared__ ChunkStart s_start;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int cta = blockIdx.x;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* sQ = reinterpret_cast<float*>(base + S::Q_OFF);
@@ -143,7 +143,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 __stcg(&d->first_row, g.rt * RT);
                 __stcg(&d->rows, min(RT, rows_all - g.rt * RT));
                 __stcg(&d->g, g.g);
-                __stcg(&d->last_cta, chunk_cta_of(s_start.total, g.item + (g.u1 - g.u0) - 1, p.num_ctas));
+                __stcg(&d->last_cta, chunk_cta_of(s_start.total, cta, g.item + (g.u1 - g.u0) - 1, p));
             }
         }
         // this warp's 8 rows of queries

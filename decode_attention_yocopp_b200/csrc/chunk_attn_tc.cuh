@@ -12,17 +12,18 @@
 //   O_x += P_x V      P from tensor memory, V MN-major from its TMA tile.
 //
 // Two shapes of a row tile, chosen by the rows that the longest chunk has:
-//   C = 0 (more than 128 rows): 256 rows, 128 in each half, every half over all
-//          128 keys of a tile.  Bound by the tensor cores and the exponentials.
-//   C = 1, 2, 4 (at most 128 / C rows): bound by the cache's bytes.  The matrix
-//          instruction has 128 rows whatever is in them, so the rows are put
-//          there 2 C times, C copies in each half: half x takes keys 64 x .. +63
-//          of every tile (N = 64 scores, K = 64 values: no product is done
-//          twice), and copy i of it forms the exponentials of 64 / C of those
-//          keys only; the other columns of its P stay zero.  The copies' results
-//          are merged at the end of a segment.  With one copy of 32 rows a
-//          single warp would form 4096 exponentials per tile, longer than the
-//          tile's bytes take; with 8 copies each warp forms 512.
+//   C = 0 (more than 128 rows): 256 rows, 128 in each half, and both halves take
+//          every key tile.  Bound by the chain of a half: its products, the
+//          softmax, its products again.
+//   C = 1, 2, 4 (at most 128 / C rows): bound by the cache's bytes.  The halves
+//          take alternate key tiles, with the same queries and each with its own
+//          maximum, sum and O.  The matrix instruction has 128 rows whatever is
+//          in them, so the rows are put there C times, and copy i forms the
+//          exponentials of keys 128 i / C .. only; the rest of its P is zero.
+//          With one copy of 32 rows a single warp would form 4096 exponentials
+//          per tile, longer than the tile's bytes take.  The 2 C results of a row
+//          are merged at the end of a segment: the halves' in registers (a warp
+//          may read both halves' O of its rows), the copies' through shared memory.
 //
 // Masked tiles.  A weight of 0 times a value that is not finite is not 0, so in
 // a tile that some row does not see whole, the value rows outside the row
@@ -48,10 +49,9 @@ struct ChunkTc {
     static constexpr bool PAIR = C == 0;
     static constexpr int RT = PAIR ? 256 : 128 / (PAIR ? 1 : C);  // rows of a row tile
     static constexpr int TK = 128;                                 // positions of a key tile
-    static constexpr int XK = PAIR ? 128 : 64;                     // keys of a half's products
-    static constexpr int NK = PAIR ? 128 : 64 / (PAIR ? 1 : C);    // keys whose exponentials a thread forms
+    static constexpr int NK = PAIR ? 128 : 128 / (PAIR ? 1 : C);   // keys whose exponentials a thread forms
     static constexpr int NBOX = D / 64, BOXB = 128 * 128, TILE_BYTES = NBOX * BOXB;
-    static constexpr int SCR_BYTES = PAIR ? 0 : 256 * 128;         // merge of the copies: 256 x 32 fp32
+    static constexpr int SCR_BYTES = PAIR ? 0 : 256 * 128;         // merge: 2 x 128 rows x 32 fp32
     static constexpr int KSLOTS = D == 64 ? 4 : (PAIR ? 2 : 3), VSLOTS = D == 64 ? 4 : 2;
     static constexpr int Q_OFF = 0;
     static constexpr int SCR_OFF = (PAIR ? 2 : 1) * TILE_BYTES;
@@ -62,10 +62,10 @@ struct ChunkTc {
     static constexpr int NBAR = 2 + 2 * KSLOTS + 2 * VSLOTS + 7;
     static constexpr int SMEM = 1024 + BAR_OFF + NBAR * 8;
     static constexpr int THREADS = 352;
-    static constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, XK, false);
+    static constexpr uint32_t IDESC_QK = umma_idesc_bf16(128, TK, false);
     static constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, true);
-    // tensor memory: S_x at 128 x (PAIR: P_x over its first 64 columns; else P_x at 128 x + 64), O_x at 256 + 128 x
-    static constexpr int TMEM_COLS = 512, P_COL = PAIR ? 0 : 64;
+    // tensor memory: S_x at 128 x, P_x over its first 64 columns, O_x at 256 + 128 x
+    static constexpr int TMEM_COLS = 512;
     static constexpr float RESCALE_SLACK = 8.f;
 };
 static_assert(ChunkTc<128, 0>::SMEM <= 232448 - 512 && ChunkTc<128, 1>::SMEM <= 232448 - 512 &&
@@ -107,11 +107,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     __shared__ volatile int s_abort;
     __shared__ int s_cdone;
     __shared__ uint32_t s_tmem;
-    __shared__ unsigned s_bad[4];          // keys of a masked tile with a value that is not finite
+    __shared__ unsigned s_bad[2][4];       // keys of a masked tile with a value that is not finite, by half
     __shared__ int64_t s_scan[S::THREADS / 32];
     __shared__ ChunkStart s_start;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int cta = blockIdx.x;
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* q_full = reinterpret_cast<uint64_t*>(base + S::BAR_OFF);  // [2]
@@ -143,8 +143,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         fence_mbar_init();
         s_abort = 0;
         s_cdone = 0;
-        s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = 0u;
     }
+    if (tid < 8) s_bad[tid >> 2][tid & 3] = 0u;
     // before the wait: nothing here depends on the previous kernel
     if (warp == 0 && lane == 0) prefetch_tensormap(&tmK);
     if (warp == 10 && lane == 0) prefetch_tensormap(&tmV);
@@ -216,96 +216,118 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 
     if (warp == 1) {
         // ------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            const uint32_t qaddr = smem_addr(base + S::Q_OFF);
-            const uint32_t kaddr = smem_addr(base + S::K_OFF);
-            const uint32_t vaddr = smem_addr(base + S::V_OFF);
-            int ks = 0, kr = 0, vs = 0, vr = 0;  // next tile's slot and round of the rings
-            int np[2] = {0, 0};                  // tiles so far of each half
-            int nq[2] = {0, 0};                  // segments so far of each half
-            bool ok = true, issued_any = false;
-            auto qk = [&](int x) {
-                const uint32_t ka = kaddr + uint32_t(ks * S::TILE_BYTES + (PAIR ? 0 : x * 64 * 128));
-                const uint32_t qa = qaddr + uint32_t(PAIR ? x * S::TILE_BYTES : 0);
+        // The whole warp runs this, one lane issues: the descriptors then are warp-uniform values, which the
+        // instruction takes as they are (computed under a divergent branch each of them is moved over first,
+        // 82 cycles per product instead of the at most 64 that the tensor pipe takes).
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t dq = umma_desc_sw128(smem_addr(base + S::Q_OFF));
+        const uint64_t dk = umma_desc_sw128(smem_addr(base + S::K_OFF));
+        const uint64_t dv = umma_desc_sw128_mn(smem_addr(base + S::V_OFF), S::BOXB, 1024);
+        const uint32_t issue = lane == 0 ? 1u : 0u;
+        int ks = 0, kr = 0, vs = 0, vr = 0;  // next tile's slot and round of the rings
+        int np[2] = {0, 0};                  // tiles so far of each half
+        int nq[2] = {0, 0};                  // segments so far of each half
+        bool ok = true;
+        auto await = [&](uint64_t* bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, !s_abort && mbar_wait(bar, parity, p.wait_limit_ns));
+        };
+        auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+        auto qk = [&](int x) {
+            const uint64_t k0 = dk + uint32_t(uni(ks) * (S::TILE_BYTES >> 4));
+            const uint64_t q0 = dq + uint32_t(PAIR ? x * (S::TILE_BYTES >> 4) : 0);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = uint32_t((kk >> 2) * S::BOXB + (kk & 3) * 32);
-                    umma_bf16(tmem + 128 * x, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off), S::IDESC_QK,
-                              kk > 0 ? 1u : 0u);
-                }
-                umma_commit(&s_full[x]);
-                issued_any = true;
-            };
-            auto pv = [&](int x, bool last) {
-                const uint32_t va = vaddr + uint32_t(vs * S::TILE_BYTES + (PAIR ? 0 : x * 64 * 128));
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = uint32_t((kk >> 2) * S::BOXB + (kk & 3) * 32) >> 4;
+                umma_bf16_by(issue, tm + 128 * x, q0 + off, k0 + off, S::IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            umma_commit_by(issue, &s_full[x]);
+        };
+        auto pv = [&](int x, bool last) {
+            const uint64_t v0 = dv + uint32_t(uni(vs) * (S::TILE_BYTES >> 4));
 #pragma unroll
-                for (int kk = 0; kk < S::XK / 16; ++kk)  // O starts from zeros that the softmax threads wrote
-                    umma_bf16_tmem_a(tmem + 256 + 128 * x, tmem + 128 * x + S::P_COL + 8 * kk,
-                                     umma_desc_sw128_mn(va + uint32_t(kk * 16 * 128), S::BOXB, 1024), S::IDESC_PV, 1u);
-                if (last) umma_commit(&o_last[x]);
-                issued_any = true;
-            };
-            auto next_k = [&]() {
-                if (++ks == S::KSLOTS) {
-                    ks = 0;
-                    ++kr;
-                }
-            };
-            while (ok && walk.next(sg)) {
-                const bool two = both(sg);
-                const int nt = sg.t1 - sg.t0;
-                ok = !s_abort && (!PAIR || mbar_wait(&q_full[0], nq[0] & 1, p.wait_limit_ns)) &&
-                     (!two || mbar_wait(&q_full[1], nq[1] & 1, p.wait_limit_ns)) &&
-                     mbar_wait(&k_full[ks], kr & 1, p.wait_limit_ns);
-                if (!ok) break;
-                ++nq[0];
-                if (two) ++nq[1];
-                tc_fence_after();
-                qk(0);
+            for (int kk = 0; kk < TK / 16; ++kk)  // O starts from zeros that the softmax threads wrote
+                umma_bf16_tmem_a_by(issue, tm + 256 + 128 * x, tm + 128 * x + 8 * kk,
+                                    v0 + uint32_t(kk * (16 * 128 >> 4)), S::IDESC_PV, 1u);
+            if (last) umma_commit_by(issue, &o_last[x]);
+        };
+        auto free_slot = [&](uint64_t* bar) {
+            umma_commit_by(issue, bar);
+        };
+        auto next_k = [&]() {
+            free_slot(&k_empty[ks]);
+            if (++ks == S::KSLOTS) {
+                ks = 0;
+                ++kr;
+            }
+        };
+        auto next_v = [&]() {
+            free_slot(&v_empty[vs]);
+            if (++vs == S::VSLOTS) {
+                vs = 0;
+                ++vr;
+            }
+        };
+        auto score = [&](int x) {  // the next key tile's scores
+            await(&k_full[ks], kr & 1);
+            tc_fence_after();
+            qk(x);
+        };
+        while (uni(walk.next(sg)) != 0) {
+            const bool two = uni(both(sg)) != 0;
+            const int nt = uni(sg.t1 - sg.t0);
+            await(&q_full[0], nq[0]++ & 1);
+            if constexpr (PAIR) {
+                if (two) await(&q_full[1], nq[1]++ & 1);
+                score(0);
                 if (two) qk(1);
-                umma_commit(&k_empty[ks]);
                 next_k();
                 for (int i = 0; i < nt; ++i) {
                     const bool more = i + 1 < nt;
                     // half 0: P V of tile i, then S of tile i + 1; the same for half 1
-                    ok = !s_abort && mbar_wait(&p_full[0], np[0]++ & 1, p.wait_limit_ns) &&
-                         mbar_wait(&v_full[vs], vr & 1, p.wait_limit_ns);
-                    if (!ok) break;
+                    await(&p_full[0], np[0]++ & 1);
+                    await(&v_full[vs], vr & 1);
                     tc_fence_after();
                     pv(0, !more);
-                    if (more) {
-                        ok = mbar_wait(&k_full[ks], kr & 1, p.wait_limit_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-                        qk(0);
-                    }
+                    if (more) score(0);
                     if (two) {
-                        ok = !s_abort && mbar_wait(&p_full[1], np[1]++ & 1, p.wait_limit_ns);
-                        if (!ok) break;
+                        await(&p_full[1], np[1]++ & 1);
                         tc_fence_after();
                         pv(1, !more);
                         if (more) qk(1);
                     }
-                    umma_commit(&v_empty[vs]);
-                    if (++vs == S::VSLOTS) {
-                        vs = 0;
-                        ++vr;
-                    }
-                    if (more) {
-                        umma_commit(&k_empty[ks]);
+                    next_v();
+                    if (more) next_k();
+                }
+            } else {
+                score(0);
+                next_k();
+                if (nt > 1) {
+                    score(1);
+                    next_k();
+                }
+                for (int i = 0; i < nt; ++i) {  // half x: P V of tile i, then S of tile i + 2
+                    const int x = i & 1;
+                    await(&p_full[x], (x ? np[1]++ : np[0]++) & 1);
+                    await(&v_full[vs], vr & 1);
+                    tc_fence_after();
+                    pv(x, i + 2 >= nt);
+                    next_v();
+                    if (i + 2 < nt) {
+                        score(x);
                         next_k();
                     }
                 }
             }
+        }
+        if (lane == 0) {
             if (!ok) {
                 record_status(YOCOPP_ETIMEOUT);
                 s_abort = 1;
             }
-            if (issued_any) {  // every product issued finishes before the tensor memory is freed
-                umma_commit(drain);
-                (void)mbar_wait(drain, 0, p.wait_limit_ns);
-            }
-            // the softmax warps finish reading O before the tensor memory is freed
+            // every product issued finishes before the tensor memory is freed
+            umma_commit(drain);
+            (void)mbar_wait(drain, 0, p.wait_limit_ns);
+            // and the softmax warps finish reading O
             const uint64_t t0 = globaltimer_ns();
             while (atomicAdd(&s_cdone, 0) < 8 && globaltimer_ns() - t0 <= p.wait_limit_ns) __nanosleep(64);
         }
@@ -319,19 +341,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int x = (warp - 2) >> 2;                  // half
     const int qd = warp & 3;
     const int r = 32 * qd + lane;                   // row of the half (tensor-memory lane)
-    const int copy = PAIR ? 0 : r / RT;             // PAIR: unused
+    const int copy = PAIR ? 0 : 32 * qd / RT;
     const int row = PAIR ? 128 * x + r : r % RT;    // row of the row tile
-    const int kofs = PAIR ? 0 : 64 * x + NK * copy; // first key of the tile that this thread takes
+    const int kofs = NK * copy;                     // first key of a tile that this thread takes
     const uint32_t lanes = uint32_t(32 * qd) << 16;
-    const uint32_t tS = tmem + 128 * x + lanes;
-    const uint32_t tP = tS + S::P_COL;
+    const uint32_t tS = tmem + 128 * x + lanes;     // this row's S, and P over it
     const uint32_t tO = tmem + 256 + 128 * x + lanes;
     uint8_t* scr = base + S::SCR_OFF;
 
-    // the queries of a segment's row tile into their swizzled tile (split: half 1 loads the one tile,
-    // whose last product is the last that half 1 has seen done)
+    // The queries of a segment's row tile into their swizzled tile: each half its own (PAIR), or the one tile
+    // by the half that had the last key tile of the segment before, and so has seen its last product done.
     auto load_q = [&](const ChunkSegment& g) {
-        if (!PAIR && x == 0) return;
         constexpr int CH = D / 8, RPI = 32 / CH, IT = 32 / RPI;  // chunks of a row, rows per pass, passes
         const int ch = lane % CH;
         const int rows_all = g.s.n * p.G;
@@ -354,15 +374,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
+        if (lane == 0) mbar_arrive(&q_full[PAIR ? x : 0]);
     };
     // The softmax warps' own barriers are named ones: all of them come to every one, whatever happens, as a
     // wait that has run out (ok = false) changes no branch around a barrier; it only makes later waits be
-    // skipped.  Barrier 1: both halves, 2: half 0 alone.
-    auto meet = [&](bool two) {
-        if (two) asm volatile("bar.sync 1, 256;" ::: "memory");
-        else asm volatile("bar.sync 2, 128;" ::: "memory");
-    };
+    // skipped.  Barrier 1: both halves, 2 and 3: one half.
+    auto meet_both = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    auto meet_half = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(2 + x) : "memory"); };
     bool ok = true;
     auto await = [&](uint64_t* bar, int parity) {
         if (ok) ok = !s_abort && mbar_wait(bar, parity, p.wait_limit_ns);
@@ -370,21 +388,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         if (!ok) s_abort = 1;
     };
 
-    if constexpr (!PAIR) {  // the columns of P that belong to other copies stay zero
-        uint32_t z[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = 0u;
-        tmem_st32u(tP, z);
-    }
-    bool split_end = false;                          // this CTA leaves its last row tile unfinished
-    int n_x = 0, n_seg = 0, vs = 0, vr = 0;
+    bool split_end = false;   // this CTA leaves its last row tile unfinished
+    int n_x = 0;              // tiles of this half so far
+    int n_o[2] = {0, 0};      // segments with tiles of either half so far
+    int tiles = 0;            // key tiles of the CTA before this segment
     bool have = walk.next(sg);
-    if (have && (x == 0 || both(sg))) load_q(sg);
+    if (have && (x == 0 || (PAIR && both(sg)))) load_q(sg);
     while (have) {
         const ChunkSegment g = sg;
         const bool two = both(g);
         const int nt = g.t1 - g.t0;
-        const bool mine = x == 0 || two;
         if (g.t0 == g.u0 && g.t1 < g.u1) {
             split_end = true;
             if (warp == 2 && lane == 0) {
@@ -393,9 +406,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 __stcg(&d->first_row, g.rt * RT);
                 __stcg(&d->rows, min(RT, g.s.n * p.G - g.rt * RT));
                 __stcg(&d->g, g.g);
-                __stcg(&d->last_cta, chunk_cta_of(s_start.total, g.item + (g.u1 - g.u0) - 1, p.num_ctas));
+                __stcg(&d->last_cta, chunk_cta_of(s_start.total, cta, g.item + (g.u1 - g.u0) - 1, p));
             }
         }
+        // this half's key tiles of the segment: all of them (PAIR), or every second
+        const int step = PAIR ? 1 : 2, i0 = PAIR ? 0 : x;
+        const bool mine = PAIR ? x == 0 || two : x < nt;
         float m_ref = NEG_INF_F, l = 0.f;
         const int R = g.rt * RT + row;               // row of the sequence
         const int rows_all = g.s.n * p.G;
@@ -415,34 +431,29 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) tmem_st32(tO + uint32_t(c * 32), z);
             }
-            for (int t = g.t0; t < g.t1; ++t) {
+            for (int i = i0; i < nt; i += step) {
                 await(&s_full[x], n_x & 1);
                 ++n_x;
                 tc_fence_after();
-                const int key0 = t * TK;
+                const int key0 = (g.t0 + i) * TK;
                 const bool masked = key0 + TK - 1 > hi_all || key0 < lo_all;
                 uint32_t u[NK];
-                if constexpr (NK == 16) {
-                    tmem_ld16_nowait(tS + uint32_t(NK * copy), u);
-                } else {
 #pragma unroll
-                    for (int c = 0; c < NK / 32; ++c)
-                        tmem_ld32_nowait(tS + uint32_t((PAIR ? 0 : NK * copy) + c * 32),
-                                         *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
-                }
+                for (int c = 0; c < NK / 32; ++c)
+                    tmem_ld32_nowait(tS + uint32_t(kofs + c * 32), *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
                 tmem_wait_ld();
                 if (masked) {
 #pragma unroll
-                    for (int w = 0; w < (NK + 31) / 32; ++w) {
+                    for (int w = 0; w < NK / 32; ++w) {
                         const uint32_t bits = sight_bits(see, key0 + kofs + 32 * w);
 #pragma unroll
-                        for (int c = 0; c < (NK < 32 ? NK : 32); ++c)
+                        for (int c = 0; c < 32; ++c)
                             if (!((bits >> c) & 1u)) u[32 * w + c] = __float_as_uint(NEG_INF_F);
                     }
                 }
                 float mx4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mx4[i] = __uint_as_float(u[i]);
+                for (int c = 0; c < 4; ++c) mx4[c] = __uint_as_float(u[c]);
 #pragma unroll
                 for (int c = 4; c < NK; c += 2)
                     mx4[(c >> 1) & 3] = fmax3_nan(mx4[(c >> 1) & 3], __uint_as_float(u[c]), __uint_as_float(u[c + 1]));
@@ -461,7 +472,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const float nmsub = m_ref == NEG_INF_F ? 0.f : -m_ref;
                 const float2 qs2 = make_float2(p.qscale, p.qscale), nm2 = make_float2(nmsub, nmsub);
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                constexpr int W = NK >= 64 ? 32 : NK / 2;  // packed pairs of one store
+                constexpr int W = NK >= 64 ? 32 : 16;  // packed pairs of one store
 #pragma unroll
                 for (int c = 0; c < NK / 2 / W; ++c) {
                     uint32_t pw[W];
@@ -469,35 +480,49 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     for (int e = 0; e < W; ++e) {
                         const int k = 2 * (W * c + e);
                         const float2 xv = ffma2(make_float2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), qs2, nm2);
-                        // a quarter of the exponentials on the FMA pipe where the tensor cores are the bound
-                        const float2 pe = PAIR && poly_pair(e) ? exp2_poly2(xv)
-                                                               : make_float2(ex2_approx(xv.x), ex2_approx(xv.y));
+                        // a quarter of the exponentials on the FMA pipe where a thread forms a whole tile's
+                        const float2 pe = NK == 128 && poly_pair(e) ? exp2_poly2(xv)
+                                                                    : make_float2(ex2_approx(xv.x), ex2_approx(xv.y));
                         pw[e] = float2_to_bf16x2(pe.x, pe.y);
                         ls[e & 1] = add_bf16x2(ls[e & 1], pw[e]);
                     }
-                    const uint32_t at = tP + uint32_t((PAIR ? 0 : NK / 2 * copy) + c * W);
+                    const uint32_t at = tS + uint32_t(kofs / 2 + c * W);
                     if constexpr (W == 32) tmem_st32u(at, pw);
-                    else if constexpr (W == 16) tmem_st16u(at, pw);
-                    else tmem_st8u(at, pw);
+                    else tmem_st16u(at, pw);
+                }
+                if constexpr (!PAIR && C > 1) {  // the other copies' keys
+                    uint32_t z[W];
+#pragma unroll
+                    for (int e = 0; e < W; ++e) z[e] = 0u;
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        if (c != copy) {
+                            if constexpr (W == 32) tmem_st32u(tS + uint32_t(c * W), z);
+                            else tmem_st16u(tS + uint32_t(c * W), z);
+                        }
                 }
                 l += (ls[0].x + ls[1].x) + (ls[0].y + ls[1].y);
-                if (t > g.t0 && __any_sync(0xffffffffu, rescale)) {
-                    // S of this tile was issued after P V of the previous one, so O is complete up to there
+                if (i > i0 && __any_sync(0xffffffffu, rescale)) {
+                    // S of this tile was issued after this half's P V of its previous one: O is complete up to there
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         float o[32];
                         tmem_ld32(tO + uint32_t(c * 32), o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= corr;
+                        for (int k = 0; k < 32; ++k) o[k] *= corr;
                         tmem_st32(tO + uint32_t(c * 32), o);
                     }
                 }
                 if (masked) {
-                    // key row r of the value tile, this half's part of its chunks
-                    await(&v_full[vs], vr & 1);
+                    // key row r of the value tile: all its chunks, or (both halves on one tile) this half's part
+                    const int vt = tiles + i, vs = vt % S::VSLOTS;
+                    await(&v_full[vs], (vt / S::VSLOTS) & 1);
                     constexpr int CH = D / 8;
-                    const int c0 = two && x == 1 ? CH / 2 : 0, c1 = two && x == 0 ? CH / 2 : CH;
-                    uint8_t* vrow = base + S::V_OFF + vs * S::TILE_BYTES + r * 128;
+                    const bool share = PAIR && two;
+                    const int c0 = share && x == 1 ? CH / 2 : 0, c1 = share && x == 0 ? CH / 2 : CH;
+                    unsigned* bits = s_bad[PAIR ? 0 : x];
+                    uint8_t* vtile = base + S::V_OFF + vs * S::TILE_BYTES;
+                    uint8_t* vrow = vtile + r * 128;
                     const bool outside = key0 + r < g.span.lo || key0 + r > g.span.hi;
                     bool bad = false;
                     for (int ch = c0; ch < c1; ++ch) {
@@ -510,75 +535,81 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                                    bf16x2_not_finite(w.w);
                         }
                     }
-                    if (bad) atomicOr(&s_bad[r >> 5], 1u << (r & 31));
-                    meet(two);
-                    const volatile unsigned* vb = s_bad;
-                    const unsigned any = vb[0] | vb[1] | vb[2] | vb[3];
-                    if (any) {  // uniform over the CTA's softmax threads
+                    if (bad) atomicOr(&bits[r >> 5], 1u << (r & 31));
+                    if (share) meet_both(); else meet_half();
+                    const volatile unsigned* vb = bits;
+                    if (vb[0] | vb[1] | vb[2] | vb[3]) {  // the same in all threads that share the tile
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[32];
                             tmem_ld32(tO + uint32_t(c * 32), o);
                             for (int k = kofs; k < kofs + NK; ++k) {
                                 if (!((vb[k >> 5] >> (k & 31)) & 1u) || !see.sees(key0 + k)) continue;
-                                const uint8_t* kr = base + S::V_OFF + vs * S::TILE_BYTES + k * 128 + (c >> 1) * S::BOXB;
+                                const uint8_t* kr = vtile + k * 128 + (c >> 1) * S::BOXB;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const int ch = (c & 1) * 4 + i / 8;
+                                for (int e = 0; e < 32; ++e) {
+                                    const int ch = (c & 1) * 4 + e / 8;
                                     const uint32_t h = *reinterpret_cast<const uint16_t*>(
-                                        kr + ((ch ^ (k & 7)) << 4) + (i & 7) * 2);
-                                    if ((h & 0x7F80u) == 0x7F80u) o[i] += __uint_as_float(h << 16);
+                                        kr + ((ch ^ (k & 7)) << 4) + (e & 7) * 2);
+                                    if ((h & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(h << 16);
                                 }
                             }
                             __syncwarp();
                             tmem_st32(tO + uint32_t(c * 32), o);
                         }
-                        meet(two);
+                        if (share) meet_both(); else meet_half();
                         if (bad) {
                             for (int ch = c0; ch < c1; ++ch) {
                                 uint16_t* a = reinterpret_cast<uint16_t*>(vrow + (ch >> 3) * S::BOXB +
                                                                           (((ch & 7) ^ (r & 7)) << 4));
-                                for (int i = 0; i < 8; ++i)
-                                    if ((a[i] & 0x7F80u) == 0x7F80u) a[i] = 0;
+                                for (int e = 0; e < 8; ++e)
+                                    if ((a[e] & 0x7F80u) == 0x7F80u) a[e] = 0;
                             }
                         }
-                        if (x == 0 && r < 4) s_bad[r] = 0u;
+                        if ((!PAIR || x == 0) && r < 4) bits[r] = 0u;
                     }
                     fence_proxy_async_smem();
-                }
-                if (++vs == S::VSLOTS) {
-                    vs = 0;
-                    ++vr;
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
             }
-        } else {
-            for (int t = 0; t < nt; ++t)
-                if (++vs == S::VSLOTS) {
-                    vs = 0;
-                    ++vr;
-                }
         }
+        tiles += nt;
         have = walk.next(sg);
-        if (have && (x == 0 || both(sg))) load_q(sg);
-        if (!mine) continue;
+        if (have && (PAIR ? x == 0 || both(sg) : x == ((nt - 1) & 1))) load_q(sg);
 
         // ---- the segment's result: whole row tiles to the output, others to the workspace
-        await(&o_last[x], n_seg & 1);
-        ++n_seg;
-        tc_fence_after();
         const bool whole = g.t0 == g.u0 && g.t1 == g.u1;
         float* slot = chunk_slot<RT, D>(p, cta, g.t0 == g.u0 ? 1 : 0);
+        // 32 channels from c * 32 of row RR of the row tile
+        auto put = [&](int RR, int c, float (&o)[32]) {
+            if (g.rt * RT + RR >= rows_all) return;
+            if (whole) {
+                const int j = chunk_token(p, g.rt * RT + RR);
+                uint8_t* orow = p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (g.rt * RT + RR - j * p.G)) *
+                                            int64_t(D * 2) + c * 64;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4)
+                    st_global(orow + q4 * 16, make_uint4(float2_to_bf16x2(o[q4 * 8 + 0], o[q4 * 8 + 1]),
+                                                         float2_to_bf16x2(o[q4 * 8 + 2], o[q4 * 8 + 3]),
+                                                         float2_to_bf16x2(o[q4 * 8 + 4], o[q4 * 8 + 5]),
+                                                         float2_to_bf16x2(o[q4 * 8 + 6], o[q4 * 8 + 7])));
+            } else {
+#pragma unroll
+                for (int q4 = 0; q4 < 8; ++q4)
+                    __stcg(reinterpret_cast<float4*>(slot + int64_t(RR) * D + c * 32 + q4 * 4),
+                           make_float4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]));
+            }
+        };
         if constexpr (PAIR) {
-            const bool store = R < rows_all;
-            const bool none = m_ref == NEG_INF_F;
-            const float w = !whole ? 1.f : none ? 0.f : 1.f / l;
-            const int j = chunk_token(p, R);
-            uint8_t* orow = p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (R - j * p.G)) * int64_t(D * 2);
-            if (!whole && store) {
+            if (!mine) continue;
+            await(&o_last[x], n_o[0]++ & 1);
+            tc_fence_after();
+            const bool none = m_ref == NEG_INF_F;   // a row that sees nothing gives zeros
+            const float w = whole ? 1.f / l : 1.f;
+            if (!whole && R < rows_all) {
                 __stcg(slot + RT * D + row, m_ref);
                 __stcg(slot + RT * D + RT + row, l);
             }
@@ -586,82 +617,91 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int c = 0; c < D / 32; ++c) {
                 float o[32];
                 tmem_ld32(tO + uint32_t(c * 32), o);
-                if (!store) continue;
-                if (whole) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * w;
-#pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4)
-                        st_global(orow + (c * 32 + q4 * 8) * 2,
-                                  make_uint4(float2_to_bf16x2(o[q4 * 8 + 0], o[q4 * 8 + 1]),
-                                             float2_to_bf16x2(o[q4 * 8 + 2], o[q4 * 8 + 3]),
-                                             float2_to_bf16x2(o[q4 * 8 + 4], o[q4 * 8 + 5]),
-                                             float2_to_bf16x2(o[q4 * 8 + 6], o[q4 * 8 + 7])));
-                } else {
-#pragma unroll
-                    for (int q4 = 0; q4 < 8; ++q4)
-                        __stcg(reinterpret_cast<float4*>(slot + int64_t(row) * D + c * 32 + q4 * 4),
-                               make_float4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]));
-                }
+                for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * w;
+                put(row, c, o);
             }
         } else {
-            constexpr int NC = 2 * (PAIR ? 1 : C);  // copies of a row
-            const int me = 128 * x + r;
             float* s_m = reinterpret_cast<float*>(scr);
             float* s_l = s_m + 256;
-            s_m[me] = m_ref;
-            s_l[me] = l;
-            meet(true);
+            s_m[128 * x + r] = m_ref;
+            s_l[128 * x + r] = l;
+            meet_both();
             float M = NEG_INF_F, L = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) M = fmaxf(M, s_m[RT * i + row]);
+            for (int k = 0; k < 2 * C; ++k) M = fmaxf(M, s_m[RT * k + row]);
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const float mi = s_m[RT * i + row];
-                L += mi == NEG_INF_F ? 0.f : s_l[RT * i + row] * ex2_approx(mi - M);
+            for (int k = 0; k < 2 * C; ++k) {
+                const float mk = s_m[RT * k + row];
+                L += mk == NEG_INF_F ? 0.f : s_l[RT * k + row] * ex2_approx(mk - M);
             }
-            meet(true);  // read by all before it is written over
-            // a row that sees nothing gives zeros
-            const float w = m_ref == NEG_INF_F ? 0.f : ex2_approx(m_ref - M) * (whole ? 1.f / L : 1.f);
+            // weights of the two halves' results in this thread's tensor-memory lane (-inf: a half without a
+            // tile, or a row that sees nothing there; its O is not looked at)
+            const float inv = whole ? 1.f / L : 1.f, ma = s_m[r], mb = s_m[128 + r];
+            const float wa = ma == NEG_INF_F ? 0.f : ex2_approx(ma - M) * inv;
+            const float wb = mb == NEG_INF_F ? 0.f : ex2_approx(mb - M) * inv;
             if (!whole && copy == 0 && x == 0 && R < rows_all) {
                 __stcg(slot + RT * D + row, M);
                 __stcg(slot + RT * D + RT + row, L);
             }
+            if (C > 1) meet_both();  // the maxima are read by all before they are written over
+            await(&o_last[0], n_o[0]++ & 1);
+            if (nt > 1) await(&o_last[1], n_o[1]++ & 1);
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int cc = 0; cc < D / 64; ++cc) {
+                const int c = x * (D / 64) + cc;  // this half writes half of the channels
                 float o[32];
-                tmem_ld32(tO + uint32_t(c * 32), o);
+                {
+                    uint32_t a[32], b[32];
+                    tmem_ld32_nowait(tmem + 256 + lanes + uint32_t(c * 32), a);
+                    tmem_ld32_nowait(tmem + 384 + lanes + uint32_t(c * 32), b);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int q4 = 0; q4 < 8; ++q4)
-                    *reinterpret_cast<float4*>(scr + me * 128 + ((q4 ^ (me & 7)) << 4)) =
-                        make_float4(o[q4 * 4] * w, o[q4 * 4 + 1] * w, o[q4 * 4 + 2] * w, o[q4 * 4 + 3] * w);
-                meet(true);
-#pragma unroll
-                for (int i = 0; i < RT / 32; ++i) {
-                    const int id = me + 256 * i, rr = id >> 3, q4 = id & 7;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < NC; ++k) {
-                        const int at = RT * k + rr;
-                        const float4 b = *reinterpret_cast<const float4*>(scr + at * 128 + ((q4 ^ (at & 7)) << 4));
-                        a.x += b.x;
-                        a.y += b.y;
-                        a.z += b.z;
-                        a.w += b.w;
-                    }
-                    const int RR = g.rt * RT + rr;
-                    if (RR >= rows_all) continue;
-                    if (whole) {
-                        const int j = chunk_token(p, RR);
-                        uint2 v = make_uint2(float2_to_bf16x2(a.x, a.y), float2_to_bf16x2(a.z, a.w));
-                        *reinterpret_cast<uint2*>(p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G + (RR - j * p.G)) *
-                                                              int64_t(D * 2) + (c * 32 + q4 * 4) * 2) = v;
-                    } else {
-                        __stcg(reinterpret_cast<float4*>(slot + int64_t(rr) * D + c * 32 + q4 * 4), a);
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = (ma == NEG_INF_F ? 0.f : __uint_as_float(a[k]) * wa) +
+                               (mb == NEG_INF_F ? 0.f : __uint_as_float(b[k]) * wb);
                 }
-                meet(true);
+                if constexpr (C == 1) {
+                    put(row, c, o);
+                } else {
+                    uint8_t* mys = scr + x * (128 * 128);
+#pragma unroll
+                    for (int q4 = 0; q4 < 8; ++q4)
+                        *reinterpret_cast<float4*>(mys + r * 128 + ((q4 ^ (r & 7)) << 4)) =
+                            make_float4(o[q4 * 4], o[q4 * 4 + 1], o[q4 * 4 + 2], o[q4 * 4 + 3]);
+                    meet_half();
+#pragma unroll
+                    for (int k = 0; k < RT * 8 / 128; ++k) {
+                        const int id = r + 128 * k, rr = id >> 3, q4 = id & 7;
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int n = 0; n < C; ++n) {
+                            const int at = RT * n + rr;
+                            const float4 b = *reinterpret_cast<const float4*>(mys + at * 128 + ((q4 ^ (at & 7)) << 4));
+                            a.x += b.x;
+                            a.y += b.y;
+                            a.z += b.z;
+                            a.w += b.w;
+                        }
+                        const int RR = g.rt * RT + rr;
+                        if (RR >= rows_all) continue;
+                        if (whole) {
+                            const int j = chunk_token(p, RR);
+                            const uint2 v = make_uint2(float2_to_bf16x2(a.x, a.y), float2_to_bf16x2(a.z, a.w));
+                            *reinterpret_cast<uint2*>(p.out + ((int64_t(g.s.row0) + j) * p.hq + g.g * p.G +
+                                                               (RR - j * p.G)) * int64_t(D * 2) + (c * 32 + q4 * 4) * 2) = v;
+                        } else {
+                            __stcg(reinterpret_cast<float4*>(slot + int64_t(rr) * D + c * 32 + q4 * 4), a);
+                        }
+                    }
+                    if (cc + 1 < D / 64) meet_half();
+                }
             }
+            // both halves have read both O before the next segment writes them, and the scratch memory
+            tc_fence_before();
+            meet_both();
+            tc_fence_after();
         }
     }
     if (!ok) record_status(YOCOPP_ETIMEOUT);

@@ -21,8 +21,6 @@ namespace yocopp {
 struct ChunkParams {
     const uint8_t* q;            // [total_q][hq][D]
     uint8_t* out;                // [total_q][hq][D]
-    const uint8_t* k;            // cache (the kernel that loads without TMA)
-    const uint8_t* v;
     const int32_t* pos;          // [batch] cache position of the first row, or null (0)
     const int32_t* cu_q;         // [batch + 1], or null (n_uniform rows each)
     const int32_t* block_table;  // null: contiguous
@@ -33,7 +31,8 @@ struct ChunkParams {
     uint32_t g_m, g_s;           // division by G (fast_div); rows of a sequence are below 2^31
     int32_t bs_log2, mbps, num_blocks, boxr;
     float qscale;                // softmax scale * log2(e)
-    int32_t num_ctas;
+    int32_t num_ctas;            // at least 2
+    uint64_t cta_m;              // ceil(2^64 / num_ctas)
     float* part;                 // [num_ctas][2][RT][D + 2]: o, then m, l
     struct ChunkDesc* desc;      // [num_ctas]
     uint64_t wait_limit_ns;
@@ -121,19 +120,17 @@ struct ChunkStart {
     int64_t item, end, total;
 };
 
-// a / b of non-negative numbers, in 32 bits (a quarter of the time) where they fit
-__device__ __forceinline__ int64_t div_items(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
-// first item of CTA c
-__device__ __forceinline__ int64_t chunk_first_item(int64_t total, int c, int num_ctas) {
-    const int64_t q = div_items(total, num_ctas), r = total - q * num_ctas;
+// first item of CTA c: total / num_ctas each, one more for the first total mod num_ctas.  The quotient by the high
+// half of the product with ceil(2^64 / num_ctas), exact for total * num_ctas < 2^64; a 64-bit division is a
+// subroutine of some hundred instructions.
+__device__ __forceinline__ int64_t chunk_first_item(const ChunkParams& p, int64_t total, int c) {
+    const int64_t q = int64_t(__umul64hi(uint64_t(total), p.cta_m)), r = total - q * p.num_ctas;
     return q * c + min(int64_t(c), r);
 }
-// the CTA that has an item
-__device__ __forceinline__ int chunk_cta_of(int64_t total, int64_t item, int num_ctas) {
-    const int64_t q = div_items(total, num_ctas), r = total - q * num_ctas;
-    return int(item < r * (q + 1) ? div_items(item, q + 1) : r + div_items(item - r * (q + 1), q));
+// the CTA that has an item, at or behind CTA c
+__device__ __forceinline__ int chunk_cta_of(int64_t total, int c, int64_t item, const ChunkParams& p) {
+    while (chunk_first_item(p, total, c + 1) <= item) ++c;
+    return c;
 }
 
 // All threads of the CTA call it; `start` is shared memory.  scan: one int64 per warp, shared.
@@ -157,7 +154,7 @@ __device__ __forceinline__ void chunk_find_start(const ChunkParams& p, int cta, 
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    const int64_t w0 = chunk_first_item(total, cta, p.num_ctas), w1 = chunk_first_item(total, cta + 1, p.num_ctas);
+    const int64_t w0 = chunk_first_item(p, total, cta), w1 = chunk_first_item(p, total, cta + 1);
     if (w0 >= w1) {
         if (tid == 0) {
             start->item = start->end = 0;
@@ -172,8 +169,9 @@ __device__ __forceinline__ void chunk_find_start(const ChunkParams& p, int cta, 
                 at += per_head * p.hkv;
                 continue;
             }
-            const int g = int(div_items(w0 - at, per_head));
-            int64_t rem = (w0 - at) - g * per_head;
+            int g = 0;
+            int64_t rem = w0 - at;
+            for (; rem >= per_head; rem -= per_head) ++g;
             int rt = 0;
             for (;; ++rt) {
                 const ChunkSpan r = chunk_span<RT>(p, s, rt);

@@ -361,7 +361,9 @@ int32_t launch_chunk(K kern, const yocopp_cache* cache, ChunkParams& p, int64_t 
     if (!encode_rows(&tk, cache->k, cache->dtype, D, cache_rows, p.boxr) ||
         !encode_rows(&tv, cache->v, cache->dtype, D, cache_rows, p.boxr))
         return YOCOPP_ECUDA;
+    if (ctas < 2) return YOCOPP_ECUDA;
     p.num_ctas = ctas;
+    p.cta_m = ~uint64_t(0) / uint64_t(ctas) + 1;
     p.desc = static_cast<ChunkDesc*>(workspace);
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + chunk_desc_bytes(ctas));
     const int32_t rc = launch_dependent(kern, dim3(unsigned(ctas)), S::THREADS, S::SMEM, st, tk, tv, p);
