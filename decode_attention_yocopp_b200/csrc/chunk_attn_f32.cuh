@@ -89,20 +89,23 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // ------------------------------------------------------------------ loader
         int issued = 0;
         bool ok = true;
+        const int nsb = TK >> p.box_log2;  // boxes of a tile
+        ChunkBoxes box;
         while (ok && walk.next(g)) {
+            box.start(p, g, g.t0 * nsb, lane);
             for (int t = g.t0; t < g.t1; ++t) {
                 const int slot = issued % S::STAGES;
-                const int crow = chunk_box_row<TK>(p, g, t, lane);
+                const int crow = box.rows(p, g, t * nsb, nsb, lane);
                 const unsigned boxes = __ballot_sync(0xffffffffu, crow >= 0);
                 if (lane == 0) ok = !s_abort && mbar_wait(&empty[slot], ((issued / S::STAGES) & 1) ^ 1, p.wait_limit_ns);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 if (!(cta == 0 && g.item + (t - g.t0) == p.drop_tile)) {  // failure injection (tests)
                     if (lane == 0)
-                        mbar_arrive_expect_tx(&full[slot], uint32_t(2 * __popc(boxes) * p.boxr * 128 * S::NBOX));
+                        mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(boxes) << p.box_log2) * (2 * 128 * S::NBOX));
                     __syncwarp();
                     if (crow >= 0) {
-                        uint8_t* dst = base + slot * S::STAGE_BYTES + lane * p.boxr * 128;
+                        uint8_t* dst = base + slot * S::STAGE_BYTES + ((lane * 128) << p.box_log2);
 #pragma unroll
                         for (int bx = 0; bx < S::NBOX; ++bx) {
                             tma_load_2d(dst + bx * S::BOXB, &tmK, &full[slot], bx * 32, crow);

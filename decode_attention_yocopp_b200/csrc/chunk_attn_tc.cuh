@@ -178,22 +178,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int slots = kl ? S::KSLOTS : S::VSLOTS;
         int slot = 0, round = 0, issued = 0;
         bool ok = true;
+        const int nsb = TK >> p.box_log2;  // boxes of a tile
+        ChunkBoxes box;
         while (ok && walk.next(sg)) {
+            box.start(p, sg, sg.t0 * nsb, lane);
             for (int t = sg.t0; t < sg.t1; ++t) {
-                // the table is read before the wait for the slot
-                const int crow = chunk_box_row<TK>(p, sg, t, lane);
+                const int crow = box.rows(p, sg, t * nsb, nsb, lane);
                 const unsigned boxes = __ballot_sync(0xffffffffu, crow >= 0);
                 if (lane == 0) ok = !s_abort && mbar_wait(&empty[slot], (round & 1) ^ 1, p.wait_limit_ns);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 if (!(kl && cta == 0 && sg.item + (t - sg.t0) == p.drop_tile)) {  // failure injection (tests)
                     if (lane == 0)
-                        mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(boxes) * p.boxr * 128 * S::NBOX));
+                        mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(boxes) << p.box_log2) * (128 * S::NBOX));
                     __syncwarp();
                     if (crow >= 0) {
 #pragma unroll
                         for (int bx = 0; bx < S::NBOX; ++bx)
-                            tma_load_2d(ring + slot * S::TILE_BYTES + bx * S::BOXB + lane * p.boxr * 128, map,
+                            tma_load_2d(ring + slot * S::TILE_BYTES + bx * S::BOXB + ((lane * 128) << p.box_log2), map,
                                         &full[slot], bx * 64, crow);
                     }
                 }

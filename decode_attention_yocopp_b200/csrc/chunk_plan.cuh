@@ -29,7 +29,7 @@ struct ChunkParams {
     int32_t n_uniform, max_q, window;
     int32_t batch, hq, hkv, G, capacity;
     uint32_t g_m, g_s;           // division by G (fast_div); rows of a sequence are below 2^31
-    int32_t bs_log2, mbps, num_blocks, boxr;
+    int32_t bs_log2, mbps, num_blocks, box_log2;
     float qscale;                // softmax scale * log2(e)
     int32_t num_ctas;            // at least 2
     uint64_t cta_m;              // ceil(2^64 / num_ctas)
@@ -261,21 +261,47 @@ __device__ __forceinline__ ChunkSight chunk_sight(const ChunkParams& p, const Ch
     return r;
 }
 
-// The boxes of key tile t, one per lane: positions t TK + lane boxr .. + boxr - 1 (one box of a contiguous
-// cache's tile, one per block of a paged one).  Gives the first cache row, or -1 where the lane has no box,
-// no row of the row tile sees it, or its block is not valid (recorded).
-template <int TK>
-__device__ __forceinline__ int chunk_box_row(const ChunkParams& p, const ChunkSegment& sg, int t, int lane) {
-    const int at = t * TK + lane * p.boxr;
-    if (lane * p.boxr >= TK || at > sg.span.hi || at + p.boxr <= sg.span.lo) return -1;
-    if (p.block_table == nullptr) return (sg.b * p.hkv + sg.g) * p.capacity + at;
-    const int blk = __ldg(p.block_table + int64_t(sg.b) * p.mbps + (at >> p.bs_log2));
-    if (blk < 0 || blk >= p.num_blocks) {
-        record_status(YOCOPP_EDEVICE_CHECK);
-        return -1;
+// The boxes of a segment's key tiles, 32 at a time, one per lane of the loading warp: box i holds positions
+// i boxr .. + boxr - 1 (the tile in a contiguous cache, one block in a paged one; boxr = 2^box_log2).  A lane
+// gives the first cache row, or -1 where no row of the row tile sees the box or its block is not valid
+// (recorded).  The table is read two windows ahead of the tiles that use it: an entry takes about 2000 cycles
+// to come from memory, longer than a tile.
+struct ChunkBoxes {
+    int base;        // first box of the window
+    int row, next;   // this lane's box of the window and of the one behind it
+    __device__ __forceinline__ int entry(const ChunkParams& p, const ChunkSegment& sg, int box) const {
+        const int at = box << p.box_log2;
+        if (at > sg.span.hi || at + (1 << p.box_log2) <= sg.span.lo) return -1;
+        if (p.block_table == nullptr) return at;
+        return __ldg(p.block_table + int64_t(sg.b) * p.mbps + (at >> p.bs_log2));
     }
-    return ((blk * p.hkv + sg.g) << p.bs_log2) + (at & ((1 << p.bs_log2) - 1));
-}
+    __device__ __forceinline__ int cache_row(const ChunkParams& p, const ChunkSegment& sg, int box, int e) const {
+        const int at = box << p.box_log2;
+        if (at > sg.span.hi || at + (1 << p.box_log2) <= sg.span.lo) return -1;
+        if (p.block_table == nullptr) return (sg.b * p.hkv + sg.g) * p.capacity + at;
+        if (e < 0 || e >= p.num_blocks) {
+            record_status(YOCOPP_EDEVICE_CHECK);
+            return -1;
+        }
+        return ((e * p.hkv + sg.g) << p.bs_log2) + (at & ((1 << p.bs_log2) - 1));
+    }
+    __device__ __forceinline__ void start(const ChunkParams& p, const ChunkSegment& sg, int box, int lane) {
+        base = box & ~31;
+        row = entry(p, sg, base + lane);
+        next = entry(p, sg, base + 32 + lane);
+        row = cache_row(p, sg, base + lane, row);
+    }
+    // the row of box `box + lane` for lane < n (n divides 32, box is a multiple of n), -1 in other lanes
+    __device__ __forceinline__ int rows(const ChunkParams& p, const ChunkSegment& sg, int box, int n, int lane) {
+        if (box >= base + 32) {
+            base += 32;
+            row = cache_row(p, sg, base + lane, next);
+            next = entry(p, sg, base + 32 + lane);
+        }
+        const int r = __shfl_sync(0xffffffffu, row, (box - base + lane) & 31);
+        return lane < n ? r : -1;
+    }
+};
 
 // Slot of the workspace for a segment that is not a whole row tile: 0 where an earlier CTA began
 // the row tile, 1 where this one did.
@@ -284,86 +310,62 @@ __device__ __forceinline__ float* chunk_slot(const ChunkParams& p, int cta, int 
     return p.part + (int64_t(cta) * 2 + which) * RT * (D + 2);
 }
 
-// Merge of the split row tiles: block (c, y) takes rows [y ROWS, ...) of the row tile that CTA c
-// began and did not finish, if there is one: the parts are CTA c's slot 1 and slot 0 of the CTAs
-// up to last_cta, merged exactly (out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i).
-constexpr int kChunkMergeRows = 8, kChunkMergeThreads = 256;
+// Merge of the split row tiles: blocks (c, *) take the rows of the row tile that CTA c began and did not finish,
+// if there is one: the parts are CTA c's slot 1 and slot 0 of the CTAs up to last_cta, merged exactly
+// (out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i), D / 4 lanes a row, 8 parts in flight.  Bound by latency:
+// the descriptor, the parts, and the instruction misses of code that runs once, so there is little of it.
+constexpr int kChunkMergeThreads = 256, kChunkMergeFan = 4;
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kChunkMergeThreads) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr int W = kChunkMergeThreads / 32, C = D / 32;
-    __shared__ float s_m[W], s_l[W], s_o[W][D];
+__global__ void __launch_bounds__(kChunkMergeThreads, 4) chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr int LPR = D / 4, ROWS = kChunkMergeThreads / LPR, F = kChunkMergeFan;
+    const float ninf = __int_as_float(0xff800000);
     griddep_wait();
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, ch = threadIdx.x % LPR;
+    const int4 d = __ldcg(reinterpret_cast<const int4*>(p.desc + c));  // row0, first_row, rows, g
     const int last = __ldcg(&p.desc[c].last_cta);
     if (last < 0) return;
-    const int rows = __ldcg(&p.desc[c].rows);
-    const int r0 = blockIdx.y * kChunkMergeRows;
-    if (r0 >= rows) return;
-    const int row0 = __ldcg(&p.desc[c].row0), first_row = __ldcg(&p.desc[c].first_row), g = __ldcg(&p.desc[c].g);
-    const int parts = last - c + 1;
-    auto part = [&](int i) { return chunk_slot<RT, D>(p, c + i, i == 0 ? 1 : 0); };
-    // parts [i0, i1) step `step` of row r by one warp: (m, l, o)
-    auto gather = [&](int r, int i0, int step, float& m, float& l, float (&o)[C]) {
-        m = __int_as_float(0xff800000);
-        l = 0.f;
+#pragma unroll 1
+    for (int r = blockIdx.y * ROWS + threadIdx.x / LPR; r < d.z; r += gridDim.y * ROWS) {
+        float M = ninf, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = c; i0 <= last; i0 += F) {
+            float m[F], l[F];
+            float4 x[F];
 #pragma unroll
-        for (int k = 0; k < C; ++k) o[k] = 0.f;
-        for (int i = i0; i < parts; i += step) {
-            const float* s = part(i);
-            const float mi = __ldcg(s + RT * D + r), li = __ldcg(s + RT * D + RT + r);
-            float x[C];
-#pragma unroll
-            for (int k = 0; k < C; ++k) x[k] = __ldcg(s + r * D + k * 32 + lane);
-            if (mi == __int_as_float(0xff800000)) continue;  // a part in which the row sees nothing
-            const float mn = fmaxf(m, mi);
-            const float a = exp2f(m - mn), e = exp2f(mi - mn);
-            m = mn;
-            l = l * a + li * e;
-#pragma unroll
-            for (int k = 0; k < C; ++k) o[k] = o[k] * a + x[k] * e;
-        }
-    };
-    auto store = [&](int r, float l, const float (&o)[C]) {
-        const int row = first_row + r, j = chunk_token(p, row);
-        const int64_t at = (int64_t(row0) + j) * p.hq + g * p.G + (row - j * p.G);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int k = 0; k < C; ++k)
-            reinterpret_cast<T*>(p.out)[at * D + k * 32 + lane] = T(l == 0.f ? 0.f : o[k] * inv);
-    };
-    float m, l, o[C];
-    if (parts < 2 * W) {  // a warp for each row
-        const int r = r0 + warp;
-        if (r >= rows) return;
-        gather(r, 0, 1, m, l, o);
-        store(r, l, o);
-        return;
-    }
-    for (int r = r0; r < min(rows, r0 + kChunkMergeRows); ++r) {  // all warps for one row
-        gather(r, warp, W, m, l, o);
-        if (lane == 0) {
-            s_m[warp] = m;
-            s_l[warp] = l;
-        }
-#pragma unroll
-        for (int k = 0; k < C; ++k) s_o[warp][k * 32 + lane] = o[k];
-        __syncthreads();
-        if (warp == 0) {
-            float M = s_m[0];
-            for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w]);
-            l = 0.f;
-#pragma unroll
-            for (int k = 0; k < C; ++k) o[k] = 0.f;
-            for (int w = 0; w < W; ++w) {
-                if (s_m[w] == __int_as_float(0xff800000)) continue;
-                const float e = exp2f(s_m[w] - M);
-                l += s_l[w] * e;
-#pragma unroll
-                for (int k = 0; k < C; ++k) o[k] += s_o[w][k * 32 + lane] * e;
+            for (int k = 0; k < F; ++k) {
+                m[k] = ninf;
+                if (i0 + k <= last) {
+                    const float* s = chunk_slot<RT, D>(p, i0 + k, i0 + k == c ? 1 : 0);
+                    m[k] = __ldcg(s + RT * D + r);
+                    l[k] = __ldcg(s + RT * D + RT + r);
+                    x[k] = __ldcg(reinterpret_cast<const float4*>(s + r * D) + ch);
+                }
             }
-            store(r, l, o);
+            float mn = M;
+#pragma unroll
+            for (int k = 0; k < F; ++k) mn = fmaxf(mn, m[k]);
+            if (mn == ninf) continue;  // parts in which the row sees nothing
+            const float a = exp2f(M - mn);
+            M = mn;
+            L *= a;
+            o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+#pragma unroll
+            for (int k = 0; k < F; ++k)
+                if (m[k] != ninf) {
+                    const float e = exp2f(m[k] - mn);
+                    L = fmaf(l[k], e, L);
+                    o = make_float4(fmaf(x[k].x, e, o.x), fmaf(x[k].y, e, o.y), fmaf(x[k].z, e, o.z), fmaf(x[k].w, e, o.w));
+                }
         }
-        __syncthreads();
+        const int row = d.y + r, j = chunk_token(p, row);
+        const float inv = M == ninf ? 0.f : 1.f / L;
+        T* out = reinterpret_cast<T*>(p.out) + ((int64_t(d.x) + j) * p.hq + d.w * p.G + (row - j * p.G)) * D + ch * 4;
+        if constexpr (Elem<T>::kBytes == 2)
+            *reinterpret_cast<uint2*>(out) = make_uint2(float2_to_bf16x2(o.x * inv, o.y * inv),
+                                                        float2_to_bf16x2(o.z * inv, o.w * inv));
+        else
+            *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
 }
 

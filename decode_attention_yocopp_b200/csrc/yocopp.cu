@@ -36,6 +36,12 @@ std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitLimitNs};
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+int ilog2(int64_t x) {
+    int n = 0;
+    while ((int64_t(1) << n) < x) ++n;
+    return n;
+}
+
 int elem_bytes(int dtype) { return dtype == YOCOPP_BF16 ? 2 : (dtype == YOCOPP_F32 ? 4 : 0); }
 
 int current_device() {
@@ -352,14 +358,18 @@ int32_t launch_chunk(K kern, const yocopp_cache* cache, ChunkParams& p, int64_t 
     const int dev = current_device();
     if (dev < 0 || dev >= kMaxDevices) return YOCOPP_ECUDA;
     if (!attr_set[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess)
+        // the merge asks for the first kernel's division of shared memory and L1, so that no SM changes it between
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(chunk_merge_kernel<T, D, S::RT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared) != cudaSuccess)
             return YOCOPP_ECUDA;
         attr_set[dev] = true;
     }
-    p.boxr = cache->block_table ? (cache->block_size < S::TK ? cache->block_size : S::TK) : S::TK;
+    const int boxr = cache->block_table && cache->block_size < S::TK ? cache->block_size : S::TK;
+    p.box_log2 = ilog2(boxr);
     alignas(64) CUtensorMap tk, tv;
-    if (!encode_rows(&tk, cache->k, cache->dtype, D, cache_rows, p.boxr) ||
-        !encode_rows(&tv, cache->v, cache->dtype, D, cache_rows, p.boxr))
+    if (!encode_rows(&tk, cache->k, cache->dtype, D, cache_rows, boxr) ||
+        !encode_rows(&tv, cache->v, cache->dtype, D, cache_rows, boxr))
         return YOCOPP_ECUDA;
     if (ctas < 2) return YOCOPP_ECUDA;
     p.num_ctas = ctas;
@@ -368,9 +378,10 @@ int32_t launch_chunk(K kern, const yocopp_cache* cache, ChunkParams& p, int64_t 
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + chunk_desc_bytes(ctas));
     const int32_t rc = launch_dependent(kern, dim3(unsigned(ctas)), S::THREADS, S::SMEM, st, tk, tv, p);
     if (rc != YOCOPP_OK) return rc;
-    const int most = rows < S::RT ? rows : S::RT;  // rows of the largest row tile
-    return launch_dependent(chunk_merge_kernel<T, D, S::RT>,
-                            dim3(unsigned(ctas), unsigned((most + kChunkMergeRows - 1) / kChunkMergeRows)),
+    // 8 (16) rows of a split row tile per block; eight blocks for one, as more of them take longer to place
+    const int most = rows < S::RT ? rows : S::RT, per = kChunkMergeThreads / (D / 4);
+    const int y = (most + per - 1) / per;
+    return launch_dependent(chunk_merge_kernel<T, D, S::RT>, dim3(unsigned(ctas), unsigned(y < 8 ? y : 8)),
                             kChunkMergeThreads, 0, st, p);
 }
 
@@ -438,12 +449,6 @@ int32_t check_pages(const yocopp_cache* c, int32_t num_caches) {
     }
     if (!aligned(c->block_table, 4)) return YOCOPP_EINVAL;
     return YOCOPP_OK;
-}
-
-int ilog2(int64_t x) {
-    int n = 0;
-    while ((int64_t(1) << n) < x) ++n;
-    return n;
 }
 
 // The table kernel (one cluster), then the copies in every layer.
