@@ -45,6 +45,7 @@ class yocopp_cache(ctypes.Structure):
 
 
 ROPE_MAX_AXES, ROPE_MAX_PAIRS = 4, 64
+_Float4 = ctypes.c_float * 4
 
 
 class yocopp_rope(ctypes.Structure):
@@ -320,32 +321,61 @@ def yocopp_chunk_attn_workspace_size(cache: yocopp_cache, num_q_heads: int) -> i
     return int(n)
 
 
-def _rows_of(q, total_q, num_q_heads):
-    return q.shape[0] if total_q is None else total_q, q.shape[1] if num_q_heads is None else num_q_heads
-
-
-def _on_device(t, name) -> None:
+# Argument checks of the chunk attention, the rotary append and the page operators.  A step of a small batch takes
+# about as long on the GPU as these wrappers take on the host, so each tensor is looked at once, with its cheapest
+# accessors, and messages are formed only when something is wrong.
+def _device() -> int:
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise TypeError(f"{name}: a tensor of the current CUDA device expected, got {t.device}")
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
-def _want(t, name, dtype) -> None:
+def _raw_stream(stream, dev: int) -> Optional[int]:
+    """The given stream, or the current one of the current device."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _bad(t, name, what):
+    where = f", on {t.device}" if not t.is_cuda or t.device.index != _device() else ""
+    return TypeError(f"{name}: {what} on the current CUDA device expected, got {t.dtype} {tuple(t.shape)}, strides "
+                     f"{tuple(t.stride())}{where}")
+
+
+def _ints(t, name, dev, dtype) -> Optional[int]:
+    """Pointer of a contiguous integer tensor."""
     if t is None:
-        return
-    if t.dtype != dtype or not t.is_contiguous():
-        raise TypeError(f"{name}: contiguous {dtype} expected, got {t.dtype}, strides {tuple(t.stride())}")
-    _on_device(t, name)
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise _bad(t, name, f"a contiguous {dtype} tensor")
+    return t.data_ptr()
 
 
-def _want_like_cache(t, name, cache) -> None:
-    """A packed [rows][heads][head_dim] tensor of the cache's type."""
+def _rows(t, name, cache, dev, like, rows) -> Optional[int]:
+    """Pointer of a packed [rows][heads][head_dim] tensor of the cache's type (`like`)."""
     if t is None:
-        return
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or _dtype_code(t) != cache.dtype or not t.is_contiguous():
-        raise TypeError(f"{name}: contiguous [rows][heads][{cache.head_dim}] of the cache's type expected, got "
-                        f"{t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}")
-    _on_device(t, name)
+        return None
+    s = t.shape
+    if (t.dtype is not like or t.get_device() != dev or len(s) != 3 or s[2] != cache.head_dim
+            or (rows is not None and s[0] != rows) or not t.is_contiguous()):
+        raise _bad(t, name, f"a contiguous [{'rows' if rows is None else rows}][heads][{cache.head_dim}] tensor of the "
+                            "cache's type")
+    return t.data_ptr()
+
+
+def _cache_type(cache):
+    import torch
+    return torch.bfloat16 if cache.dtype == YOCOPP_BF16 else torch.float32
+
+
+def _space(t, name, dev):
+    """Pointer and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise _bad(t, name, "a contiguous tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def yocopp_chunk_attn(q, cache: yocopp_cache, out, workspace, pos=None, cu_q=None, n_uniform: int = 0,
@@ -355,20 +385,19 @@ def yocopp_chunk_attn(q, cache: yocopp_cache, out, workspace, pos=None, cu_q=Non
     last ``window`` positions, or, with ``tree_mask`` (int64 [total_q], bit c = the row sees the chunk's row c), over
     everything cached before the chunk and the marked rows of it.  out like q."""
     import torch
-    total_q, hq = _rows_of(q, total_q, num_q_heads)
-    _want_like_cache(q, "q", cache)
-    _want_like_cache(out, "out", cache)
+    if q is None or out is None:
+        raise TypeError("q and out are needed")
+    dev, like = _device(), _cache_type(cache)
+    pq, po = _rows(q, "q", cache, dev, like, None), _rows(out, "out", cache, dev, like, q.shape[0])
     if out.shape != q.shape:
-        raise TypeError(f"out: {tuple(q.shape)} expected, got {tuple(out.shape)}")
-    _want(pos, "pos", torch.int32)
-    _want(cu_q, "cu_q", torch.int32)
-    _want(tree_mask, "tree_mask", torch.int64)
-    rc = load().yocopp_chunk_attn(_ptr(q), ctypes.byref(cache), _ptr(pos), _ptr(cu_q), int(n_uniform), int(total_q),
-                                  int(max_q), _ptr(tree_mask), int(window), _ptr(out), int(hq), float(scale),
-                                  _ptr(workspace),
-                                  workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                  _stream(stream))
-    _check("yocopp_chunk_attn", rc)
+        raise _bad(out, "out", f"a tensor of q's shape {tuple(q.shape)}")
+    ws, size = _space(workspace, "workspace", dev)
+    rc = (_lib or load()).yocopp_chunk_attn(
+        pq, cache, _ints(pos, "pos", dev, torch.int32), _ints(cu_q, "cu_q", dev, torch.int32), n_uniform,
+        q.shape[0] if total_q is None else total_q, max_q, _ints(tree_mask, "tree_mask", dev, torch.int64), window, po,
+        q.shape[1] if num_q_heads is None else num_q_heads, scale, ws, size, _raw_stream(stream, dev))
+    if rc:
+        _check("yocopp_chunk_attn", rc)
 
 
 def alloc_chunk_workspace(cache: yocopp_cache, num_q_heads: int, device=None):
@@ -409,25 +438,25 @@ def yocopp_rope_compose_append(K1, V1, Ki, Vi, alpha: Optional[Sequence[float]],
     """yocopp_compose_append with the keys turned by their tokens' positions (int32 [num_axes][total_new]), and the
     queries q [total_new][hq][d] turned into q_out (which may be q).  K1 = V1 = Ki = Vi = None: queries only."""
     import torch
-    a = None if alpha is None else (ctypes.c_float * 4)(*[float(x) for x in alpha])
     if total_new is None:
         total_new = K1.shape[0] if K1 is not None else q.shape[0] if q is not None else 0
-    for name, t in (("K1", K1), ("V1", V1), ("Ki", Ki), ("Vi", Vi), ("q", q), ("q_out", q_out)):
-        _want_like_cache(t, name, cache)
-        if t is not None and t.shape[0] != total_new:
-            raise TypeError(f"{name}: {total_new} rows expected, got {t.shape[0]}")
+    dev, like, n = _device(), _cache_type(cache), total_new
     if q is not None and q_out is not None and q.shape != q_out.shape:
-        raise TypeError(f"q_out: {tuple(q.shape)} expected, got {tuple(q_out.shape)}")
-    if positions is not None and tuple(positions.shape) != (rope.num_axes, total_new):
-        raise TypeError(f"positions: [{rope.num_axes}][{total_new}] expected, got {tuple(positions.shape)}")
-    _want(positions, "positions", torch.int32)
-    _want(pos, "pos", torch.int32)
-    _want(cu_new, "cu_new", torch.int32)
-    rc = load().yocopp_rope_compose_append(_ptr(K1), _ptr(V1), _ptr(Ki), _ptr(Vi), a, float(lam), ctypes.byref(rope),
-                                           _ptr(positions), ctypes.byref(cache), _ptr(pos), _ptr(q), _ptr(q_out),
-                                           int(q.shape[1]) if q is not None else 0, _ptr(cu_new), int(n_uniform),
-                                           int(total_new), _stream(stream))
-    _check("yocopp_rope_compose_append", rc)
+        raise _bad(q_out, "q_out", f"a tensor of q's shape {tuple(q.shape)}")
+    for name, t in (("K1", K1), ("V1", V1), ("Ki", Ki), ("Vi", Vi)):
+        if t is not None and t.shape[1:2] != (cache.num_kv_heads,):
+            raise _bad(t, name, f"a [{n}][{cache.num_kv_heads}][{cache.head_dim}] tensor")
+    if positions is not None and positions.shape != (rope.num_axes, n):
+        raise _bad(positions, "positions", f"a [{rope.num_axes}][{n}] tensor")
+    rc = (_lib or load()).yocopp_rope_compose_append(
+        _rows(K1, "K1", cache, dev, like, n), _rows(V1, "V1", cache, dev, like, n), _rows(Ki, "Ki", cache, dev, like, n),
+        _rows(Vi, "Vi", cache, dev, like, n), None if alpha is None else _Float4(*alpha), lam, rope,
+        _ints(positions, "positions", dev, torch.int32), cache, _ints(pos, "pos", dev, torch.int32),
+        _rows(q, "q", cache, dev, like, n), _rows(q_out, "q_out", cache, dev, like, n),
+        q.shape[1] if q is not None else 0, _ints(cu_new, "cu_new", dev, torch.int32), n_uniform, n,
+        _raw_stream(stream, dev))
+    if rc:
+        _check("yocopp_rope_compose_append", rc)
 
 
 def cache_list(caches: Sequence[yocopp_cache]):
@@ -450,44 +479,53 @@ def alloc_pages_workspace(caches, device=None):
     return torch.empty(yocopp_pages_workspace_size(caches), dtype=torch.uint8, device=device or "cuda")
 
 
-def _pages_args(caches, refs, workspace, **requests) -> int:
+def _pages_refs(caches, refs, dev):
     import torch
-    _want(refs, "refs", torch.int32)
     if refs is not None and refs.numel() != caches[0].num_blocks:
-        raise TypeError(f"refs: {caches[0].num_blocks} counts expected, got {refs.numel()}")
-    n = min((t.numel() for t in requests.values()), default=0)
-    for name, t in requests.items():
-        _want(t, name, torch.int32)
-        if t.numel() != n:
-            raise TypeError(f"{name}: {n} entries expected, got {t.numel()}")
-    return n
+        raise _bad(refs, "refs", f"a tensor of {caches[0].num_blocks} counts")
+    return _ints(refs, "refs", dev, torch.int32)
+
+
+def _requests(t, name, dev, n):
+    import torch
+    if t.numel() != n:
+        raise _bad(t, name, f"a tensor of {n} entries")
+    return _ints(t, name, dev, torch.int32)
 
 
 def yocopp_pages_resize(caches, refs, seqs, lens, held, workspace, stream=None) -> None:
     """Table row seqs[i] is to hold lens[i] tokens: blocks are added or taken back, and a shared last block that is
     kept in part is replaced by a copy.  held[i] = the blocks it holds then, or -1 where there were too few."""
-    n = _pages_args(caches, refs, workspace, seqs=seqs, lens=lens, held=held)
-    rc = load().yocopp_pages_resize(caches, len(caches), _ptr(refs), _ptr(seqs), _ptr(lens), n, _ptr(held),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("yocopp_pages_resize", rc)
+    dev, n = _device(), seqs.numel()
+    ws, size = _space(workspace, "workspace", dev)
+    rc = (_lib or load()).yocopp_pages_resize(caches, len(caches), _pages_refs(caches, refs, dev),
+                                              _requests(seqs, "seqs", dev, n), _requests(lens, "lens", dev, n), n,
+                                              _requests(held, "held", dev, n), ws, size, _raw_stream(stream, dev))
+    if rc:
+        _check("yocopp_pages_resize", rc)
 
 
 def yocopp_pages_fork(caches, refs, src, dst, lens, held, workspace, deep: bool = False, stream=None) -> None:
     """Empty table row dst[i] gets the first lens[i] tokens of row src[i]: full blocks shared and a part of one
     copied, or (deep) all copied."""
-    n = _pages_args(caches, refs, workspace, src=src, dst=dst, lens=lens, held=held)
-    rc = load().yocopp_pages_fork(caches, len(caches), _ptr(refs), _ptr(src), _ptr(dst), _ptr(lens), n,
-                                  1 if deep else 0, _ptr(held), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("yocopp_pages_fork", rc)
+    dev, n = _device(), src.numel()
+    ws, size = _space(workspace, "workspace", dev)
+    rc = (_lib or load()).yocopp_pages_fork(caches, len(caches), _pages_refs(caches, refs, dev),
+                                            _requests(src, "src", dev, n), _requests(dst, "dst", dev, n),
+                                            _requests(lens, "lens", dev, n), n, 1 if deep else 0,
+                                            _requests(held, "held", dev, n), ws, size, _raw_stream(stream, dev))
+    if rc:
+        _check("yocopp_pages_fork", rc)
 
 
 def yocopp_pages_compact(caches, refs, live, workspace, stream=None) -> None:
     """Move the blocks in use to the front of every layer's pool; live[0] = how many there are."""
-    _pages_args(caches, refs, workspace, live=live)
-    rc = load().yocopp_pages_compact(caches, len(caches), _ptr(refs), _ptr(live), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("yocopp_pages_compact", rc)
+    dev = _device()
+    ws, size = _space(workspace, "workspace", dev)
+    rc = (_lib or load()).yocopp_pages_compact(caches, len(caches), _pages_refs(caches, refs, dev),
+                                               _requests(live, "live", dev, 1), ws, size, _raw_stream(stream, dev))
+    if rc:
+        _check("yocopp_pages_compact", rc)
 
 
 STATIC_SCRATCH_BYTES = 4 << 20  # size of the library's fixed scratch array (include/yocopp.h)

@@ -44,10 +44,6 @@ struct PagesParams {
     int4* req;             // [n] have, need, want (-1: refused), first place in `order`
 };
 
-__device__ __forceinline__ void cluster_sync() {
-    __threadfence();
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -57,6 +53,13 @@ __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
+}
+
+// Barrier of all the cluster's threads; what they wrote to global memory before it is there for the others'
+// loads from L2 behind it (release and acquire at cluster scope, or the block's barrier where it is alone).
+__device__ __forceinline__ void cluster_sync() {
+    if (cluster_size() == 1) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Exclusive prefix sum over the block's threads; `total` gets the sum.
@@ -136,13 +139,21 @@ __device__ __forceinline__ int count_segment(const int32_t* refs, Segment s) {
 template <bool FREE, typename F>
 __device__ __forceinline__ void visit_segment(const int32_t* refs, Segment s, int before, F visit) {
     const int lane = threadIdx.x & 31;
-    for (int i = s.lo; i < s.hi; i += 32) {
-        const int id = i + lane;
-        const int r = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
-        const bool is = FREE ? r == 0 : r > 0;
-        const unsigned m = __ballot_sync(0xffffffffu, is);
-        if (id < s.hi) visit(id, is, before + __popc(m & ((1u << lane) - 1u)));
-        before += __popc(m);
+    for (int i = s.lo; i < s.hi; i += 32 * 8) {
+        int r[8];  // loads in flight together
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int id = i + 32 * k + lane;
+            r[k] = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int id = i + 32 * k + lane;
+            const bool is = FREE ? r[k] == 0 : r[k] > 0;
+            const unsigned m = __ballot_sync(0xffffffffu, is);
+            if (id < s.hi) visit(id, is, before + __popc(m & ((1u << lane) - 1u)));
+            before += __popc(m);
+        }
     }
 }
 
@@ -220,6 +231,9 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
     } else {
         // a row named by two requests belongs to the first
         const int32_t* target = OP == kPagesFork ? p.b : p.a;
+        // this warp's first request, read while the CTA finds out whose each row is
+        const int row0 = warp < p.n ? __ldcg(target + warp) : -1, len0 = warp < p.n ? __ldcg(p.lens + warp) : 0;
+        const int src0 = OP == kPagesFork && warp < p.n ? __ldcg(p.a + warp) : -1;
         for (int i = tid; i < p.batch; i += kPagesThreads) first[i] = p.n;
         __syncthreads();
         for (int i = tid; i < p.n; i += kPagesThreads) {
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
         __syncthreads();
         // each request by a warp: what its row holds and what it needs; resize releases what it no longer needs
         for (int i = warp; i < p.n; i += warps) {
-            const int row = __ldcg(target + i), len = __ldcg(p.lens + i);
+            const int row = i == warp ? row0 : __ldcg(target + i), len = i == warp ? len0 : __ldcg(p.lens + i);
             int4 q = make_int4(0, 0, -1, 0);
             int bad = 0;
             if (row < 0 || row >= p.batch || first[row] != i) bad = YOCOPP_EDEVICE_CHECK;
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                     }
                     q.z = max(0, q.y - q.x);
                 } else {
-                    const int src = __ldcg(p.a + i);
+                    const int src = i == warp ? src0 : __ldcg(p.a + i);
                     if (src < 0 || src >= p.batch || src == row || __ldcg(entries) >= 0) {
                         bad = YOCOPP_EDEVICE_CHECK;
                     } else {
@@ -306,11 +320,13 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 if (is && rank < want_all) __stcg(p.order + rank, id);
             });
         cluster_sync();
-        for (int i = warp; i < p.n; i += warps) {
+        // each request by as many warps as there are for it
+        const int per = max(1, warps / p.n), part = warp / p.n;
+        for (int i = warp % p.n; part < per && i < p.n; i += per == 1 ? warps : p.n) {
             const int4 q = __ldcg(p.req + i);
             const int len = __ldcg(p.lens + i);
             const bool given = q.z == 0 || (q.z > 0 && q.w >= 0);
-            if (lane == 0) {
+            if (part == 0 && lane == 0) {
                 p.held[i] = given ? q.y : -1;
                 if (q.z > 0 && q.w < 0) record_status(YOCOPP_ECAPACITY);
             }
@@ -319,12 +335,12 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 if (q.z == 0) continue;
                 int32_t* entries = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
                 if (q.y > q.x) {
-                    for (int k = lane; k < q.z; k += 32) {
+                    for (int k = part * 32 + lane; k < q.z; k += per * 32) {
                         const int id = __ldcg(p.order + q.w + k);
                         entries[q.x + k] = id;
                         p.refs[id] = 1;
                     }
-                } else if (lane == 0) {
+                } else if (part == 0 && lane == 0) {
                     const int old = __ldcg(entries + q.y - 1), id = __ldcg(p.order + q.w);
                     entries[q.y - 1] = id;
                     p.refs[id] = 1;
@@ -335,7 +351,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 const int32_t* from = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
                 int32_t* entries = p.table + int64_t(__ldcg(p.b + i)) * p.mbps;
                 const int shared = q.y - q.z;
-                for (int k = lane; k < q.y; k += 32) {
+                for (int k = part * 32 + lane; k < q.y; k += per * 32) {
                     int id = __ldcg(from + k);
                     if (id < 0 || id >= p.num_blocks) {
                         record_status(YOCOPP_EDEVICE_CHECK);
@@ -352,7 +368,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                     }
                 }
                 // the copies are the places given out: as many as the last request that got any
-                if (lane == 0 && q.z > 0) atomicMax(p.count, q.w + q.z);
+                if (part == 0 && lane == 0 && q.z > 0) atomicMax(p.count, q.w + q.z);
             }
         }
     }
