@@ -21,6 +21,8 @@ constexpr int kPagesMaxLayers = 128;
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesMaxRequests = 8192;  // = the largest batch
 constexpr int kPagesMaxCluster = 8;
+constexpr int kPagesAloneBlocks = 8192, kPagesAloneRequests = 32;
+static_assert(kPagesAloneBlocks <= kPagesMaxRequests, "the free list takes the place of the row owners");
 constexpr int kCopyThreads = 256;
 
 enum { kPagesResize = 0, kPagesFork = 1, kPagesCompact = 2 };
@@ -56,10 +58,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 
 // Barrier of all the cluster's threads; what they wrote to global memory before it is there for the others'
-// loads from L2 behind it (release and acquire at cluster scope, or the block's barrier where it is alone).
+// loads from L2 behind it (release and acquire at cluster scope).
 __device__ __forceinline__ void cluster_sync() {
-    if (cluster_size() == 1) __syncthreads();
-    else asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Exclusive prefix sum over the block's threads; `total` gets the sum.
@@ -105,63 +106,75 @@ __device__ __forceinline__ int row_held(const int32_t* row, int mbps) {
     return lo;
 }
 
-// The free (FREE) or used blocks of [0, num_blocks), counted by warps over contiguous segments.
-// body(id, rank) is called for every such block with its rank among them.  Two calls of the
-// pair count / visit; `before` is the number in front of this CTA's part.
-struct Segment {
-    int lo, hi;
-};
-__device__ __forceinline__ Segment warp_segment(int nb) {
-    const int warps = int(cluster_size()) * (kPagesThreads / 32);
-    const int w = int(cluster_rank()) * (kPagesThreads / 32) + (threadIdx.x >> 5);
-    const int per = ((nb + warps - 1) / warps + 31) & ~31;
-    return Segment{min(nb, w * per), min(nb, (w + 1) * per)};
-}
+// The free (FREE) or used blocks of [0, num_blocks): each warp has a segment of them, whose first 256 counts
+// stay in its registers from the count to the visit.
 template <bool FREE>
-__device__ __forceinline__ int count_segment(const int32_t* refs, Segment s) {
-    const int lane = threadIdx.x & 31;
-    int n = 0;
-    for (int i = s.lo; i < s.hi; i += 32 * 8) {
-        int r[8];
+struct Segment {
+    static constexpr int K = 8;  // loads in flight
+    const int32_t* refs;
+    int lo, hi;
+    int r[K];
+    __device__ __forceinline__ void load(int i, int (&x)[K]) const {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < K; ++k) {
             const int id = i + 32 * k + lane;
-            r[k] = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) n += FREE ? r[k] == 0 : r[k] > 0;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
-}
-// visit(id, is, rank): every block of the segment, whether it is one that counts, and how many count before it
-template <bool FREE, typename F>
-__device__ __forceinline__ void visit_segment(const int32_t* refs, Segment s, int before, F visit) {
-    const int lane = threadIdx.x & 31;
-    for (int i = s.lo; i < s.hi; i += 32 * 8) {
-        int r[8];  // loads in flight together
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int id = i + 32 * k + lane;
-            r[k] = id < s.hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int id = i + 32 * k + lane;
-            const bool is = FREE ? r[k] == 0 : r[k] > 0;
-            const unsigned m = __ballot_sync(0xffffffffu, is);
-            if (id < s.hi) visit(id, is, before + __popc(m & ((1u << lane) - 1u)));
-            before += __popc(m);
+            x[k] = id < hi ? __ldcg(refs + id) : (FREE ? 1 : 0);
         }
     }
-}
+    static __device__ __forceinline__ bool is(int x) { return FREE ? x == 0 : x > 0; }
+    // issues the loads of the first 256
+    __device__ __forceinline__ void begin(const int32_t* refs_, int nb, int warp, int warps) {
+        refs = refs_;
+        const int per = ((nb + warps - 1) / warps + 31) & ~31;
+        lo = min(nb, warp * per);
+        hi = min(nb, lo + per);
+        load(lo, r);
+    }
+    __device__ __forceinline__ int count() const {
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) n += is(r[k]);
+#pragma unroll 1
+        for (int i = lo + 32 * K; i < hi; i += 32 * K) {
+            int x[K];
+            load(i, x);
+#pragma unroll
+            for (int k = 0; k < K; ++k) n += is(x[k]);
+        }
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+    // visit(id, is, rank): every block of the segment, whether it counts, and how many count before it
+    template <typename F>
+    __device__ __forceinline__ void visit(int before, F f) const {
+        const int lane = threadIdx.x & 31;
+        auto batch = [&](int i, const int (&x)[K]) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int id = i + 32 * k + lane;
+                const unsigned m = __ballot_sync(0xffffffffu, is(x[k]));
+                if (id < hi) f(id, is(x[k]), before + __popc(m & ((1u << lane) - 1u)));
+                before += __popc(m);
+            }
+        };
+        batch(lo, r);
+#pragma unroll 1
+        for (int i = lo + 32 * K; i < hi; i += 32 * K) {
+            int x[K];
+            load(i, x);
+            batch(i, x);
+        }
+    }
+};
 
 // Counts before each warp's segment: the block's scan of the warps' counts plus the counts of
 // the CTAs in front, which go through the workspace.  The cluster barrier is inside.
+template <bool ALONE>
 __device__ __forceinline__ int cluster_before(int mine, int32_t* totals, int* warp_sums, int& total) {
     int cta;
-    const int before = block_scan((threadIdx.x & 31) == 0 ? mine : 0, warp_sums, cta);
+    const int before = __shfl_sync(0xffffffffu, block_scan((threadIdx.x & 31) == 0 ? mine : 0, warp_sums, cta), 0);
+    total = cta;
+    if (ALONE) return before;
     if (threadIdx.x == 0) __stcg(totals + cluster_rank(), cta);
     cluster_sync();
     int add = 0;
@@ -171,46 +184,61 @@ __device__ __forceinline__ int cluster_before(int mine, int32_t* totals, int* wa
         if (r < int(cluster_rank())) add += t;
         total += t;
     }
-    return __shfl_sync(0xffffffffu, before, 0) + add;
+    return before + add;
 }
 
-template <int OP>
+// ALONE: one CTA, at most kPagesAloneBlocks blocks and kPagesAloneRequests requests, whose state stays in shared
+// memory (a round trip to L2 is about 700 cycles, and the phases depend on one another).  Otherwise a
+// cluster, and the state in the workspace.  Measured for 8 requests over 160 blocks: 14300 cycles with the
+// state in the workspace.
+template <int OP, bool ALONE>
 __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __grid_constant__ PagesParams p) {
-    __shared__ int first[OP == kPagesCompact ? 1 : kPagesMaxRequests];  // first request that names a row
+    constexpr bool REQUESTS = OP != kPagesCompact;
+    __shared__ int first[REQUESTS ? kPagesMaxRequests : 1];  // first request that names a row; ALONE: then the free blocks
+    __shared__ int4 s_req[REQUESTS && ALONE ? kPagesAloneRequests : 1];
+    __shared__ int s_count;
     __shared__ int warp_sums[32];
     __shared__ int64_t warp_sums64[32];
     griddep_launch_dependents();  // the copy kernel's CTAs may take their places; they wait for this kernel's end
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int warps = int(cluster_size()) * (kPagesThreads / 32);
-    const int warp = int(cluster_rank()) * (kPagesThreads / 32) + (tid >> 5);
-    const bool lead = cluster_rank() == 0;
+    const int ctas = ALONE ? 1 : int(cluster_size()), rank = ALONE ? 0 : int(cluster_rank());
+    const int warps = ctas * (kPagesThreads / 32), warp = rank * (kPagesThreads / 32) + (tid >> 5);
+    const bool lead = rank == 0;
     const int bs = 1 << p.bs_log2;
-    if (lead && tid == 0) __stcg(p.count, 0);
+    auto sync = [&]() {
+        if (ALONE) __syncthreads();
+        else cluster_sync();
+    };
 
     if constexpr (OP == kPagesCompact) {
-        const Segment seg = warp_segment(p.num_blocks);
+        Segment<false> seg;
+        seg.begin(p.refs, p.num_blocks, warp, warps);
         int live;
-        const int before = cluster_before(count_segment<false>(p.refs, seg), p.totals, warp_sums, live);
+        const int before = cluster_before<ALONE>(seg.count(), p.totals, warp_sums, live);
         // live blocks below `live`: counted up to there by the warp whose segment holds that place
         if (live >= seg.lo && live < seg.hi) {
             int below = before;
-            visit_segment<false>(p.refs, Segment{seg.lo, live}, before,
-                                 [&](int, bool is, int rank) { below = rank + is; });
-            // the last block visited by the highest lane has the count
+            seg.visit(before, [&](int id, bool is, int rank) {
+                if (id < live) below = rank + is;
+            });
             below = __reduce_max_sync(0xffffffffu, below);
-            if (lane == 0) __stcg(p.count + 2, below);
+            if (lane == 0) {
+                if (ALONE) s_count = below;
+                else __stcg(p.count + 2, below);
+            }
         } else if (live == p.num_blocks && lead && tid == 0) {
-            __stcg(p.count + 2, live);
+            if (ALONE) s_count = live;
+            else __stcg(p.count + 2, live);
         }
         if (lead && tid == 0) {
             __stcg(p.count + 1, live);
             p.held[0] = live;
         }
-        cluster_sync();
-        const int below = __ldcg(p.count + 2);
+        sync();
+        const int below = ALONE ? s_count : __ldcg(p.count + 2);
         const int moves = live - below;
-        visit_segment<false>(p.refs, seg, before, [&](int id, bool used, int rank) {
+        seg.visit(before, [&](int id, bool used, int rank) {
             if (id < live) {
                 if (!used) __stcg(p.order + (id - rank), id);
             } else {
@@ -218,7 +246,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 else __stcg(p.remap + id, -1);
             }
         });
-        cluster_sync();
+        sync();
         for (int k = warp * 32 + lane; k < moves; k += warps * 32) {
             const int src = __ldcg(p.order2 + k), dst = __ldcg(p.order + k);
             p.copies[k] = make_int4(src, dst, bs, 0);
@@ -229,11 +257,22 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
         if (lead && tid == 0) __stcg(p.count, moves);
         return;
     } else {
+        // have, need, want (-1: refused), and first a resize's last entry, then the first place in the free list
+        auto get_req = [&](int i) { return ALONE ? s_req[i] : __ldcg(p.req + i); };
+        auto set_req = [&](int i, int4 q) {
+            if (ALONE) s_req[i] = q;
+            else __stcg(p.req + i, q);
+        };
+        auto place = [&](int at) { return ALONE ? first[at] : __ldcg(p.order + at); };
         // a row named by two requests belongs to the first
         const int32_t* target = OP == kPagesFork ? p.b : p.a;
         // this warp's first request, read while the CTA finds out whose each row is
         const int row0 = warp < p.n ? __ldcg(target + warp) : -1, len0 = warp < p.n ? __ldcg(p.lens + warp) : 0;
         const int src0 = OP == kPagesFork && warp < p.n ? __ldcg(p.a + warp) : -1;
+        if (lead && tid == 0) {
+            if (ALONE) s_count = 0;
+            else __stcg(p.count, 0);
+        }
         for (int i = tid; i < p.batch; i += kPagesThreads) first[i] = p.n;
         __syncthreads();
         for (int i = tid; i < p.n; i += kPagesThreads) {
@@ -244,7 +283,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
         // each request by a warp: what its row holds and what it needs; resize releases what it no longer needs
         for (int i = warp; i < p.n; i += warps) {
             const int row = i == warp ? row0 : __ldcg(target + i), len = i == warp ? len0 : __ldcg(p.lens + i);
-            int4 q = make_int4(0, 0, -1, 0);
+            int4 q = make_int4(0, 0, -1, -1);
             int bad = 0;
             if (row < 0 || row >= p.batch || first[row] != i) bad = YOCOPP_EDEVICE_CHECK;
             else if (len < 0 || int64_t(len) > int64_t(p.mbps) << p.bs_log2) bad = YOCOPP_ECAPACITY;
@@ -252,18 +291,30 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 q.y = int((int64_t(len) + bs - 1) >> p.bs_log2);
                 int32_t* entries = p.table + int64_t(row) * p.mbps;
                 if constexpr (OP == kPagesResize) {
+                    const int tail = q.y > 0 ? __ldcg(entries + q.y - 1) : -1;
                     q.x = row_held(entries, p.mbps);
-                    for (int e = q.y + lane; e < q.x; e += 32) {
-                        const int id = __ldcg(entries + e);
-                        if (id < 0 || id >= p.num_blocks) {
-                            record_status(YOCOPP_EDEVICE_CHECK);
-                        } else if (atomicSub(p.refs + id, 1) <= 0) {  // counted less often than it is named
-                            atomicAdd(p.refs + id, 1);
-                            record_status(YOCOPP_EDEVICE_CHECK);
+                    for (int e0 = q.y + lane; e0 < q.x; e0 += 32 * 4) {
+                        int id[4], old[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) id[k] = e0 + 32 * k < q.x ? __ldcg(entries + e0 + 32 * k) : -1;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            old[k] = 1;
+                            if (e0 + 32 * k >= q.x) continue;
+                            if (id[k] < 0 || id[k] >= p.num_blocks) record_status(YOCOPP_EDEVICE_CHECK);
+                            else old[k] = atomicSub(p.refs + id[k], 1);
+                            __stcg(entries + e0 + 32 * k, -1);
                         }
-                        __stcg(entries + e, -1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (old[k] <= 0) {  // counted less often than it is named
+                                atomicAdd(p.refs + id[k], 1);
+                                record_status(YOCOPP_EDEVICE_CHECK);
+                            }
                     }
                     q.z = max(0, q.y - q.x);
+                    // a last page that is kept in part is replaced by a copy if it is still shared then
+                    if ((len & (bs - 1)) && q.y <= q.x && tail < p.num_blocks) q.w = tail;
                 } else {
                     const int src = i == warp ? src0 : __ldcg(p.a + i);
                     if (src < 0 || src >= p.batch || src == row || __ldcg(entries) >= 0) {
@@ -279,51 +330,64 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 q.z = -1;
                 if (lane == 0) record_status(bad);
             }
-            if (lane == 0) __stcg(p.req + i, q);
+            if (lane == 0) set_req(i, q);
         }
-        cluster_sync();
-        // resize: a last page that is kept in part and still shared is replaced by a copy
+        sync();
+        Segment<true> seg;
+        seg.begin(p.refs, p.num_blocks, warp, warps);
         if constexpr (OP == kPagesResize) {
-            for (int i = int(cluster_rank()) * kPagesThreads + tid; i < p.n; i += int(cluster_size()) * kPagesThreads) {
-                int4 q = __ldcg(p.req + i);
-                const int len = __ldcg(p.lens + i);
-                if (q.z >= 0 && (len & (bs - 1)) && q.y <= q.x) {
-                    const int id = __ldcg(p.table + int64_t(__ldcg(p.a + i)) * p.mbps + q.y - 1);
-                    if (id >= 0 && id < p.num_blocks && __ldcg(p.refs + id) > 1) {
-                        q.z = 1;
-                        __stcg(p.req + i, q);
-                    }
+            for (int i = rank * kPagesThreads + tid; i < p.n; i += ctas * kPagesThreads) {
+                int4 q = get_req(i);
+                if (q.z >= 0 && q.w >= 0 && __ldcg(p.refs + q.w) > 1) {
+                    q.z = 1;
+                    set_req(i, q);
                 }
             }
         }
-        const Segment seg = warp_segment(p.num_blocks);
         int spare;
-        const int before = cluster_before(count_segment<true>(p.refs, seg), p.totals, warp_sums, spare);
-        // every CTA sums the requests' wants in order (the first CTA writes their places)
+        const int before = cluster_before<ALONE>(seg.count(), p.totals, warp_sums, spare);
         int64_t run = 0;
-        for (int i0 = 0; i0 < p.n; i0 += kPagesThreads) {
-            const int i = i0 + tid;
-            int4 q = i < p.n ? __ldcg(p.req + i) : make_int4(0, 0, 0, 0);
-            int64_t sum;
-            const int64_t at = block_scan(int64_t(max(0, q.z)), warp_sums64, sum);
-            if (lead && i < p.n) {
-                const int64_t base = run + at;
-                // places past the spare blocks: refused
-                q.w = base + max(0, q.z) <= spare ? int(base) : -1;
-                __stcg(p.req + i, q);
+        if constexpr (ALONE) {
+            // every warp sums the requests' wants in order; the first writes their places
+            const int4 q = lane < p.n ? s_req[lane] : make_int4(0, 0, 0, 0);
+            const int w = max(0, q.z);
+            int sum = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
             }
-            run += sum;
+            run = __shfl_sync(0xffffffffu, sum, 31);
+            __syncwarp();
+            if (tid < p.n) s_req[tid].w = sum <= spare ? sum - w : -1;
+        } else {
+            // every CTA sums the requests' wants in order (the first CTA writes their places)
+            for (int i0 = 0; i0 < p.n; i0 += kPagesThreads) {
+                const int i = i0 + tid;
+                int4 q = i < p.n ? __ldcg(p.req + i) : make_int4(0, 0, 0, 0);
+                int64_t sum;
+                const int64_t at = block_scan(int64_t(max(0, q.z)), warp_sums64, sum);
+                if (lead && i < p.n) {
+                    const int64_t base = run + at;
+                    q.w = base + max(0, q.z) <= spare ? int(base) : -1;  // places past the spare blocks: refused
+                    __stcg(&p.req[i].w, q.w);
+                }
+                run += sum;
+            }
         }
         const int want_all = int(min(run, int64_t(spare)));
         if (before < want_all)
-            visit_segment<true>(p.refs, seg, before, [&](int id, bool is, int rank) {
-                if (is && rank < want_all) __stcg(p.order + rank, id);
+            seg.visit(before, [&](int id, bool is, int rank) {
+                if (is && rank < want_all) {
+                    if (ALONE) first[rank] = id;
+                    else __stcg(p.order + rank, id);
+                }
             });
-        cluster_sync();
+        sync();
         // each request by as many warps as there are for it
         const int per = max(1, warps / p.n), part = warp / p.n;
         for (int i = warp % p.n; part < per && i < p.n; i += per == 1 ? warps : p.n) {
-            const int4 q = __ldcg(p.req + i);
+            const int4 q = get_req(i);
             const int len = __ldcg(p.lens + i);
             const bool given = q.z == 0 || (q.z > 0 && q.w >= 0);
             if (part == 0 && lane == 0) {
@@ -336,16 +400,16 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                 int32_t* entries = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
                 if (q.y > q.x) {
                     for (int k = part * 32 + lane; k < q.z; k += per * 32) {
-                        const int id = __ldcg(p.order + q.w + k);
+                        const int id = place(q.w + k);
                         entries[q.x + k] = id;
                         p.refs[id] = 1;
                     }
                 } else if (part == 0 && lane == 0) {
-                    const int old = __ldcg(entries + q.y - 1), id = __ldcg(p.order + q.w);
+                    const int old = __ldcg(entries + q.y - 1), id = place(q.w);
                     entries[q.y - 1] = id;
                     p.refs[id] = 1;
                     atomicSub(p.refs + old, 1);
-                    p.copies[atomicAdd(p.count, 1)] = make_int4(old, id, len & (bs - 1), 0);
+                    p.copies[atomicAdd(ALONE ? &s_count : p.count, 1)] = make_int4(old, id, len & (bs - 1), 0);
                 }
             } else {
                 const int32_t* from = p.table + int64_t(__ldcg(p.a + i)) * p.mbps;
@@ -361,15 +425,19 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_table_kernel(const __g
                         if (id >= 0) atomicAdd(p.refs + id, 1);
                         entries[k] = id;
                     } else {
-                        const int at = q.w + k - shared, to = __ldcg(p.order + at);
+                        const int at = q.w + k - shared, to = place(at);
                         entries[k] = to;
                         p.refs[to] = 1;
                         p.copies[at] = make_int4(id < 0 ? to : id, to, id < 0 ? 0 : min(bs, len - (k << p.bs_log2)), 0);
                     }
                 }
                 // the copies are the places given out: as many as the last request that got any
-                if (part == 0 && lane == 0 && q.z > 0) atomicMax(p.count, q.w + q.z);
+                if (part == 0 && lane == 0 && q.z > 0) atomicMax(ALONE ? &s_count : p.count, q.w + q.z);
             }
+        }
+        if (ALONE) {
+            __syncthreads();
+            if (tid == 0) __stcg(p.count, s_count);
         }
     }
 }

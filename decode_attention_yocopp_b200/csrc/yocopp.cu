@@ -476,7 +476,8 @@ int32_t launch_pages(const yocopp_cache* caches, int32_t num_caches, PagesParams
     if (sms <= 0) return YOCOPP_ECUDA;
     // one CTA settles small pools and few requests (a cluster barrier between CTAs costs more than it
     // saves there); eight share large ones
-    const int cluster = c->num_blocks <= 8192 && (OP == kPagesCompact || p.n <= 32) ? 1 : kPagesMaxCluster;
+    const bool alone = c->num_blocks <= kPagesAloneBlocks && p.n <= kPagesAloneRequests;
+    const int cluster = alone ? 1 : kPagesMaxCluster;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(unsigned(cluster), 1, 1);
     lc.blockDim = dim3(kPagesThreads, 1, 1);
@@ -490,7 +491,8 @@ int32_t launch_pages(const yocopp_cache* caches, int32_t num_caches, PagesParams
     attr[1].val.clusterDim.z = 1;
     lc.attrs = attr;
     lc.numAttrs = 2;
-    const int32_t rc = cuda_status(cudaLaunchKernelEx(&lc, pages_table_kernel<OP>, p));
+    const int32_t rc = cuda_status(alone ? cudaLaunchKernelEx(&lc, pages_table_kernel<OP, true>, p)
+                                         : cudaLaunchKernelEx(&lc, pages_table_kernel<OP, false>, p));
     if (rc != YOCOPP_OK) return rc;
 
     CopyParams q = {};
