@@ -39,6 +39,7 @@ struct RopeParams {
     const int32_t* positions;    // [axes][total]
     int64_t total;
     int32_t hq, pairs, tokens;   // tokens: tokens of one table in this launch
+    uint32_t turned_m, turned_s, hq_m, hq_s, pairs_m, pairs_s;  // division by the items of a turned row, hq, pairs (fast_div)
     double turns[kRopeMaxPairs];  // inv_freq / (2 pi)
     uint8_t axis[kRopeMaxPairs];
 };
@@ -77,6 +78,12 @@ template <> struct Chunk16<float> {
     }
 };
 
+// Items of a row that is turned: pairs of chunks, chunks, or (kRopeAny) single pairs and channels.
+enum { kRopeHalves = 0, kRopeInterleaved = 1, kRopeAny = 2 };
+__host__ __device__ inline int rope_items(int layout, int pairs, int n, int cpr, int d) {
+    return layout == kRopeHalves ? cpr - pairs / n : layout == kRopeInterleaved ? cpr : d - pairs;
+}
+
 // fp32 composition of one 16-byte chunk (not rounded to the cache type)
 template <typename T>
 __device__ __forceinline__ void compose_f32(uint4 a1, uint4 ai, const ComposeCoef& c, float (&f)[Chunk16<T>::N]) {
@@ -108,10 +115,9 @@ template <> __device__ __forceinline__ void store1<float>(uint8_t* p, float x) {
 //                     thread takes the two chunks that hold the same pairs;
 //   kRopeInterleaved  (2c, 2c + 1): a thread takes one chunk;
 //   kRopeAny          (c, c + pairs) for every other count: a thread takes a pair.
-enum { kRopeHalves = 0, kRopeInterleaved = 1, kRopeAny = 2 };
 
 template <typename T, int D, int LAYOUT>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_append_kernel(const __grid_constant__ RopeParams p) {
     constexpr int N = Chunk16<T>::N, ROWB = D * Elem<T>::kBytes, CPR = ROWB / 16;
     __shared__ float2 tab[kRopeTokens][kRopeMaxPairs];
     __shared__ int64_t dst_row[kRopeTokens];  // cache row of the token's first KV head, or -1
@@ -122,13 +128,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int pairs = p.pairs;
     const ComposeCoef ck = make_coef(c.ak1, c.ak2, c.lam), cv = make_coef(c.av1, c.av2, c.lam);
     const int64_t head_rows = c.block_table == nullptr ? c.capacity : c.block_size;
-    // items of one row that is turned: pairs of chunks, chunks, or single pairs and channels
-    const int turned = LAYOUT == kRopeHalves ? pairs / N + (CPR - 2 * (pairs / N))
-                     : LAYOUT == kRopeInterleaved ? CPR : pairs + (D - 2 * pairs);
+    const int turned = rope_items(LAYOUT, pairs, N, CPR, D);
     for (int64_t t0 = int64_t(blockIdx.x) * p.tokens; t0 < p.total; t0 += int64_t(gridDim.x) * p.tokens) {
         const int nt = int(min(int64_t(p.tokens), p.total - t0));
         for (int i = tid; i < nt * pairs; i += kRopeThreads) {
-            const int t = i / pairs, k = i % pairs;
+            const int t = fast_div(i, p.pairs_m, p.pairs_s), k = i - t * pairs;
             const int x = __ldg(p.positions + int64_t(p.axis[k]) * p.total + t0 + t);
             double turn = double(x) * p.turns[k];
             turn -= rint(turn);
@@ -217,8 +221,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 
         if (append) {
             for (int i = tid; i < nt * c.hkv * turned; i += kRopeThreads) {
-                const int row = i / turned, item = i % turned;
-                const int t = row / c.hkv, h = row % c.hkv;
+                const int row = fast_div(i, p.turned_m, p.turned_s), item = i - row * turned;
+                const int t = fast_div(row, c.hkv_m, c.hkv_s), h = row - t * c.hkv;
                 if (dst_row[t] < 0) continue;
                 const int64_t in = ((t0 + t) * c.hkv + h) * ROWB;
                 uint8_t* out = c.ck + (dst_row[t] + h * head_rows) * ROWB;
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
             }
             for (int i = tid; i < nt * c.hkv * CPR; i += kRopeThreads) {
                 const int row = i / CPR, off = (i % CPR) * 16;
-                const int t = row / c.hkv, h = row % c.hkv;
+                const int t = fast_div(row, c.hkv_m, c.hkv_s), h = row - t * c.hkv;
                 if (dst_row[t] < 0) continue;
                 const int64_t in = ((t0 + t) * c.hkv + h) * ROWB + off;
                 st_global(c.cv + (dst_row[t] + h * head_rows) * ROWB + off,
@@ -251,13 +255,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
         if (p.q != nullptr) {
             // q may be turned in place: a thread reads all that it writes, and nobody else reads it
             for (int i = tid; i < nt * p.hq * turned; i += kRopeThreads) {
-                const int row = i / turned, item = i % turned;
+                const int row = fast_div(i, p.turned_m, p.turned_s), item = i - row * turned;
                 const int64_t in = (t0 * p.hq + row) * ROWB;
                 if constexpr (LAYOUT == kRopeAny) {
-                    turn_any(row / p.hq, item, [&](int off) { return load1<T>(p.q + in + off); },
+                    turn_any(fast_div(row, p.hq_m, p.hq_s), item, [&](int off) { return load1<T>(p.q + in + off); },
                              [&](int off, float x) { store1<T>(p.qo + in + off, x); });
                 } else {
-                    turn_row(row / p.hq, item,
+                    turn_row(fast_div(row, p.hq_m, p.hq_s), item,
                              [&](int off, float (&f)[N]) {
                                  Chunk16<T>::unpack(*reinterpret_cast<const uint4*>(p.q + in + off), f);
                              },

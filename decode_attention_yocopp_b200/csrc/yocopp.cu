@@ -408,13 +408,25 @@ int32_t launch_chunk_any(const yocopp_cache* cache, ChunkParams& p, int64_t cach
 // ---------------------------------------------------------------- rotary append
 template <typename T, int D>
 int32_t launch_rope(RopeParams& p, bool interleaved, int sms, cudaStream_t st) {
-    // tables of as many tokens as leave every SM two CTAs' worth, four at most
+    // a CTA for each table (one wave of CTAs that loop measured 6% slower: the tokens' time varies with the pages)
+    // of four tokens, or of one where there are too few tokens to fill the SMs
     p.tokens = p.total >= int64_t(sms) * 8 ? kRopeTokens : 1;
     int64_t grid = (p.total + p.tokens - 1) / p.tokens;
-    if (grid > int64_t(sms) * 8) grid = int64_t(sms) * 8;
     const dim3 g{unsigned(grid)};
-    if (interleaved) return launch_dependent(rope_append_kernel<T, D, kRopeInterleaved>, g, kRopeThreads, 0, st, p);
-    if (p.pairs % Chunk16<T>::N == 0) return launch_dependent(rope_append_kernel<T, D, kRopeHalves>, g, kRopeThreads, 0, st, p);
+    const int layout = interleaved ? kRopeInterleaved : p.pairs % Chunk16<T>::N == 0 ? kRopeHalves : kRopeAny;
+    const FastDiv dt = make_fast_div(uint32_t(rope_items(layout, p.pairs, Chunk16<T>::N, D * Elem<T>::kBytes / 16, D)));
+    const FastDiv dk = make_fast_div(uint32_t(p.c.hkv)), dq = make_fast_div(uint32_t(p.hq > 0 ? p.hq : 1));
+    const FastDiv dp = make_fast_div(uint32_t(p.pairs));
+    p.turned_m = dt.m;
+    p.turned_s = dt.s;
+    p.c.hkv_m = dk.m;
+    p.c.hkv_s = dk.s;
+    p.hq_m = dq.m;
+    p.hq_s = dq.s;
+    p.pairs_m = dp.m;
+    p.pairs_s = dp.s;
+    if (layout == kRopeInterleaved) return launch_dependent(rope_append_kernel<T, D, kRopeInterleaved>, g, kRopeThreads, 0, st, p);
+    if (layout == kRopeHalves) return launch_dependent(rope_append_kernel<T, D, kRopeHalves>, g, kRopeThreads, 0, st, p);
     return launch_dependent(rope_append_kernel<T, D, kRopeAny>, g, kRopeThreads, 0, st, p);
 }
 
