@@ -165,10 +165,6 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             }
             __syncwarp();
         }
-        ChunkSight see[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            see[i] = chunk_sight(p, g.s, min(chunk_token(p, g.rt * RT + row0 + i), g.s.n - 1));
         const int j0 = chunk_token(p, g.rt * RT);
         const int j1 = min(chunk_token(p, g.rt * RT + RT - 1), g.s.n - 1);
         const int hi_all = p.tree ? g.s.p0 - 1 : g.s.p0 + j0;
@@ -217,6 +213,15 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                         a[i][k] = ffma2(make_float2(q[i].z, q[i].w), make_float2(kk[k].z, kk[k].w), a[i][k]);
                     }
             }
+            if (masked) {  // what a row sees is looked up here, as it would hold 28 registers through the loop
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ChunkSight see = chunk_sight(p, g.s, min(chunk_token(p, g.rt * RT + row0 + i), g.s.n - 1));
+#pragma unroll
+                    for (int k = 0; k < KP; ++k)
+                        if (!see.sees(key0 + (C == 1 ? tx + 16 * k : 16 * copy + tx))) a[i][k] = make_float2(NEG_INF_F, NEG_INF_F);
+                }
+            }
             // ---- weights against the running maximum
             float corr[4];
 #pragma unroll
@@ -224,9 +229,7 @@ chunk_f32_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 float s[KP], mx = NEG_INF_F;
 #pragma unroll
                 for (int k = 0; k < KP; ++k) {
-                    const int key = C == 1 ? tx + 16 * k : 16 * copy + tx;
                     s[k] = (a[i][k].x + a[i][k].y) * p.qscale;
-                    if (masked && !see[i].sees(key0 + key)) s[k] = NEG_INF_F;
                     mx = fmaxf(mx, s[k]);
                 }
 #pragma unroll
