@@ -1104,7 +1104,9 @@ int32_t yocopp_rope_compose_append(const void* K1, const void* V1, const void* K
     }
     if ((q == nullptr) != (q_out == nullptr)) return YOCOPP_EINVAL;
     if (!any && q == nullptr && total_new > 0) return YOCOPP_EINVAL;  // nothing to turn
-    if (q != nullptr && (num_q_heads < 1 || !aligned(q, 16) || !aligned(q_out, 16))) return YOCOPP_EINVAL;
+    if (q != nullptr && (num_q_heads < 1 || num_q_heads > (1 << 20) || !aligned(q, 16) || !aligned(q_out, 16)))
+        return YOCOPP_EINVAL;
+    if (cache->num_kv_heads > (1 << 20)) return YOCOPP_EINVAL;  // items of a token stay 32-bit
     if (total_new == 0) return YOCOPP_OK;
     const int sms = sm_count(current_device());
     if (sms <= 0) return YOCOPP_ECUDA;

@@ -16,8 +16,10 @@ from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
-from . import (alloc_workspace, make_cache, yocopp_compose_append, yocopp_decode_attn, yocopp_prefill_attn,
-               yocopp_prefill_compose_attn, yocopp_prefill_compose_attn_workspace_size)
+from . import (alloc_chunk_workspace, alloc_pages_workspace, alloc_workspace, cache_list, make_cache, yocopp_chunk_attn,
+               yocopp_compose_append, yocopp_decode_attn, yocopp_pages_compact, yocopp_pages_fork, yocopp_pages_resize,
+               yocopp_prefill_attn, yocopp_prefill_compose_attn, yocopp_prefill_compose_attn_workspace_size,
+               yocopp_rope_compose_append, yocopp_rope)
 
 LAMBDA = 35.0
 
@@ -108,3 +110,65 @@ class SharedKVStack:
                                     num_q_heads=self.hq, scale=scale, stream=stream)
         return out
 
+    # ---- positions on several axes, chunks over what is cached
+    def write_rope(self, i: int, K1, V1, Ki, Vi, rope: yocopp_rope, positions: torch.Tensor, pos: torch.Tensor,
+                   q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                   cu_new: Optional[torch.Tensor] = None, n_uniform: int = 0, stream=None) -> None:
+        """``write`` with the keys, and the layer's queries q into q_out, turned by the tokens' positions
+        (int32 [axes][tokens]; raw K1 and Ki are given unturned)."""
+        yocopp_rope_compose_append(K1, V1, Ki, Vi, self.layer_alpha(i), self.lam, rope, positions, self.desc[i], pos,
+                                   q=q, q_out=q_out, cu_new=cu_new, n_uniform=n_uniform, stream=stream)
+
+    def turn_queries(self, q: torch.Tensor, rope: yocopp_rope, positions: torch.Tensor,
+                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """A cross-decoder layer's queries turned by their tokens' positions (in place without ``out``)."""
+        out = q if out is None else out
+        yocopp_rope_compose_append(None, None, None, None, None, self.lam, rope, positions,
+                                   self.desc[self.shared_layer], None, q=q, q_out=out, stream=stream)
+        return out
+
+    def chunk_attend(self, i: int, q: torch.Tensor, out: torch.Tensor, pos: Optional[torch.Tensor] = None,
+                     cu_q: Optional[torch.Tensor] = None, n_uniform: int = 0, max_q: int = 0,
+                     tree_mask: Optional[torch.Tensor] = None, window: int = 0, scale: float = 0.0,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of new tokens over layer i's cache (self-decoder layer i, or with i = the shared layer any
+        cross-decoder layer), causal, windowed or tree-masked.  Calls on several streams at once need a workspace
+        each."""
+        if workspace is None:
+            if getattr(self, "_chunk_ws", None) is None:
+                self._chunk_ws = alloc_chunk_workspace(self.desc[i], self.hq, device=self.device)
+            workspace = self._chunk_ws
+        yocopp_chunk_attn(q, self.desc[i], out, workspace, pos=pos, cu_q=cu_q, n_uniform=n_uniform, max_q=max_q,
+                          tree_mask=tree_mask, window=window, num_q_heads=self.hq, scale=scale, stream=stream)
+        return out
+
+    # ---- pages of the paged caches (all cached layers share the block table)
+    def start_pages(self) -> None:
+        """Empty every row of the block table; from here on the page calls below settle it."""
+        if self.block_table is None:
+            raise ValueError("contiguous caches have no pages")
+        self.block_table.fill_(-1)
+        caches = [self.desc[i] for i in sorted(self.desc)]
+        self._pages = cache_list(caches)
+        self.block_refs = torch.zeros(caches[0].num_blocks, dtype=torch.int32, device=self.device)
+        self._pages_ws = alloc_pages_workspace(self._pages, device=self.device)
+
+    def resize_pages(self, seqs: torch.Tensor, lens: torch.Tensor, held: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+        """Rows seqs are to hold lens tokens each; blocks held by each afterwards, -1 where there were too few."""
+        held = torch.empty_like(seqs) if held is None else held
+        yocopp_pages_resize(self._pages, self.block_refs, seqs, lens, held, self._pages_ws, stream=stream)
+        return held
+
+    def fork_pages(self, src: torch.Tensor, dst: torch.Tensor, lens: torch.Tensor, deep: bool = False,
+                   held: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Empty rows dst get the first lens tokens of rows src, full blocks shared (or, deep, all copied)."""
+        held = torch.empty_like(src) if held is None else held
+        yocopp_pages_fork(self._pages, self.block_refs, src, dst, lens, held, self._pages_ws, deep=deep, stream=stream)
+        return held
+
+    def compact_pages(self, live: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The blocks in use to the front of every layer's pool; how many there are."""
+        live = torch.empty(1, dtype=torch.int32, device=self.device) if live is None else live
+        yocopp_pages_compact(self._pages, self.block_refs, live, self._pages_ws, stream=stream)
+        return live

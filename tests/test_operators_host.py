@@ -75,7 +75,7 @@ def test_rope_descriptor_refusals(rope):
 @pytest.mark.parametrize("kw", [
     dict(raw=(None, 0x10, 0x10, 0x10)), dict(raw=(0x10, 0x10, 0x10, None)), dict(raw=(0x10, 0x18, 0x10, 0x10)),
     dict(alpha=None), dict(alpha=(float("inf"), 0, 0, 0)), dict(lam=float("nan")), dict(positions=None), dict(pos=None),
-    dict(q=None), dict(qo=None), dict(q=0x28), dict(qo=0x38), dict(hq=0), dict(n=2), dict(total=-1), dict(total=1 << 31),
+    dict(q=None), dict(qo=None), dict(q=0x28), dict(qo=0x38), dict(hq=0), dict(hq=(1 << 20) + 1), dict(n=2), dict(total=-1), dict(total=1 << 31),
     dict(raw=(None,) * 4, q=None, qo=None), dict(c=_cache(head_dim=64))])
 def test_rope_refusals(kw):
     assert _rope_call(_bad_rope(), **kw) == y.YOCOPP_EINVAL
