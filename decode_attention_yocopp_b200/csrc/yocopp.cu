@@ -344,11 +344,9 @@ int32_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned threads, size_t
 int64_t chunk_desc_bytes(int64_t ctas) { return int64_t(up256(size_t(ctas) * sizeof(ChunkDesc))); }
 int64_t chunk_slot_bytes(int rows, int D) { return int64_t(2) * rows * (D + 2) * int64_t(sizeof(float)); }
 
-// The widest of the launches that a cache and head count can get.
+// The widest of the launches that a cache can get (one CTA per SM in each).
 int64_t chunk_workspace_bytes(const yocopp_cache* c, int sms) {
-    if (c->dtype == YOCOPP_BF16) return chunk_desc_bytes(sms) + sms * chunk_slot_bytes(256, c->head_dim);
-    const int64_t ctas = int64_t(sms) * (c->head_dim == 64 ? ChunkF32<64, 1>::CTAS_PER_SM : ChunkF32<128, 1>::CTAS_PER_SM);
-    return chunk_desc_bytes(ctas) + ctas * chunk_slot_bytes(64, c->head_dim);
+    return chunk_desc_bytes(sms) + sms * chunk_slot_bytes(c->dtype == YOCOPP_BF16 ? 256 : 64, c->head_dim);
 }
 
 template <typename S, typename T, int D, typename K>
@@ -390,9 +388,8 @@ int32_t launch_chunk_any(const yocopp_cache* cache, ChunkParams& p, int64_t cach
                          void* workspace, cudaStream_t st) {
 #define YOCOPP_CHUNK_TC(CC) \
     return launch_chunk<ChunkTc<D, CC>, __nv_bfloat16, D>(chunk_tc_kernel<D, CC>, cache, p, cache_rows, rows, sms, workspace, st)
-#define YOCOPP_CHUNK_F32(CC)                                                                                     \
-    return launch_chunk<ChunkF32<D, CC>, float, D>(chunk_f32_kernel<D, CC>, cache, p, cache_rows, rows,          \
-                                                   sms * ChunkF32<D, CC>::CTAS_PER_SM, workspace, st)
+#define YOCOPP_CHUNK_F32(CC) \
+    return launch_chunk<ChunkF32<D, CC>, float, D>(chunk_f32_kernel<D, CC>, cache, p, cache_rows, rows, sms, workspace, st)
     if (cache->dtype == YOCOPP_BF16) {
         if (rows <= 32) YOCOPP_CHUNK_TC(4);
         if (rows <= 64) YOCOPP_CHUNK_TC(2);
