@@ -22,6 +22,10 @@
 // writes two rows and the queries once.  The sines of a token serve all of its
 // heads: a CTA first forms the table of a few tokens in shared memory, then
 // streams their rows in 16-byte chunks, a thread taking both chunks of a pair.
+// Measured: 8 x 4096 tokens, 32 query and 8 KV heads of 128 bf16 channels, 120 us
+// (5.7 TB/s, 87% of the measured copy rate); 32 tokens 5 us.  Threads that take a
+// chunk of all four tokens at once, with 8 loads in flight each, were slower
+// (205 us: 128 registers, a quarter of the warps).
 #pragma once
 
 #include "compose_append.cuh"

@@ -359,11 +359,9 @@ int32_t yocopp_prefill_compose_attn(const void* K1, const void* V1, const void* 
  *     window.
  * A row that sees nothing (pos 0 and an empty word) gives zeros.  What lies at
  * positions a row does not see never reaches its output, NaN and infinities
- * included; a score of +inf or NaN makes its whole row NaN.  Positions that no
- * row of a row tile sees are not read, block by block, so a sequence's blocks
- * below every window may have been released (entries -1), at 256 positions'
- * grain: blocks that hold no position from (first window's start rounded down
- * to 128) on.
+ * included; a score of +inf or NaN makes its whole row NaN.  A block that holds
+ * no position that some row sees is not read, nor is its table entry: the blocks
+ * below the first row's window may have been released.
  * Scores, softmax statistics and sums are fp32; with bf16 the probabilities are
  * rounded to bf16 for the value product (2^-9 relative each at most, shared by
  * the row sum).

@@ -186,6 +186,12 @@ def test_causal(y, dtype, d, rows, G):
     Case(y, dtype=dtype, d=d, G=G, rows=rows, pos=[100 + 61 * i for i in range(len(rows))], block=32, seed=2).check(y)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,rows", [(40, [1, 3]), (129, [2]), (300, [1, 2])])
+def test_many_query_heads_for_one_kv_head(y, dtype, G, rows):
+    Case(y, dtype=dtype, d=64, hkv=1, G=G, rows=rows, pos=[150, 7][: len(rows)], block=16, seed=2).check(y)
+
+
 @pytest.mark.parametrize("dtype,d", TYPES)
 @pytest.mark.parametrize("block", [0, 16, 32, 64, 128, 256])
 def test_layouts_and_context_edges(y, dtype, d, block):
@@ -361,13 +367,14 @@ def test_a_wait_that_runs_out_is_recorded(y, dtype, rows):
     c.check(y)
 
 
-def test_released_blocks_below_the_window(y):
-    c = Case(y, rows=[20], pos=[700], window=100, block=16, seed=18)
+@pytest.mark.parametrize("dtype,rows", [("bf16", 20), ("bf16", 70), ("f32", 20), ("f32", 3)])
+def test_released_blocks_below_the_window(y, dtype, rows):
+    c = Case(y, dtype=dtype, rows=[rows], pos=[700], window=100, block=16, seed=18)
     ref = c.check(y)
-    # the first window starts at 601, its key tile at 512
-    blocks = c.table[0, : 512 // 16].long()
+    gone = 601 // 16  # blocks wholly below the first window, which starts at 601
+    blocks = c.table[0, :gone].long()
     c.k[blocks], c.v[blocks] = float("nan"), float("nan")
-    c.table[0, : 512 // 16] = -1
+    c.table[0, :gone] = -1
     assert torch.equal(c.check(y), ref)
 
 
