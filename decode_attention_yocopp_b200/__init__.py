@@ -343,13 +343,20 @@ def _bad(t, name, what):
                      f"{tuple(t.stride())}{where}")
 
 
-def _ints(t, name, dev, dtype) -> Optional[int]:
-    """Pointer of a contiguous integer tensor."""
+def _ints(t, name, dev, dtype, least: int = 0) -> Optional[int]:
+    """Pointer of a contiguous integer tensor of at least so many entries."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise _bad(t, name, f"a contiguous {dtype} tensor")
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < least or not t.is_contiguous():
+        raise _bad(t, name, f"a contiguous {dtype} tensor of {least} entries or more")
     return t.data_ptr()
+
+
+def _cache_here(cache, dev) -> None:
+    """A cache made of tensors lies on the current device."""
+    keep = getattr(cache, "_keep", None)
+    if keep and keep[0].get_device() != dev:
+        raise _bad(keep[0], "cache", "its tensors")
 
 
 def _rows(t, name, cache, dev, like, rows) -> Optional[int]:
@@ -388,14 +395,18 @@ def yocopp_chunk_attn(q, cache: yocopp_cache, out, workspace, pos=None, cu_q=Non
     if q is None or out is None:
         raise TypeError("q and out are needed")
     dev, like = _device(), _cache_type(cache)
+    _cache_here(cache, dev)
+    total_q = q.shape[0] if total_q is None else total_q
+    if total_q > q.shape[0] or (num_q_heads is not None and num_q_heads != q.shape[1]):
+        raise _bad(q, "q", f"a tensor of {total_q} rows and {num_q_heads or 'any number of'} heads")
     pq, po = _rows(q, "q", cache, dev, like, None), _rows(out, "out", cache, dev, like, q.shape[0])
     if out.shape != q.shape:
         raise _bad(out, "out", f"a tensor of q's shape {tuple(q.shape)}")
     ws, size = _space(workspace, "workspace", dev)
     rc = (_lib or load()).yocopp_chunk_attn(
-        pq, cache, _ints(pos, "pos", dev, torch.int32), _ints(cu_q, "cu_q", dev, torch.int32), n_uniform,
-        q.shape[0] if total_q is None else total_q, max_q, _ints(tree_mask, "tree_mask", dev, torch.int64), window, po,
-        q.shape[1] if num_q_heads is None else num_q_heads, scale, ws, size, _raw_stream(stream, dev))
+        pq, cache, _ints(pos, "pos", dev, torch.int32, cache.batch), _ints(cu_q, "cu_q", dev, torch.int32, cache.batch + 1),
+        n_uniform, total_q, max_q, _ints(tree_mask, "tree_mask", dev, torch.int64, total_q), window, po, q.shape[1], scale,
+        ws, size, _raw_stream(stream, dev))
     if rc:
         _check("yocopp_chunk_attn", rc)
 
@@ -441,6 +452,7 @@ def yocopp_rope_compose_append(K1, V1, Ki, Vi, alpha: Optional[Sequence[float]],
     if total_new is None:
         total_new = K1.shape[0] if K1 is not None else q.shape[0] if q is not None else 0
     dev, like, n = _device(), _cache_type(cache), total_new
+    _cache_here(cache, dev)
     if q is not None and q_out is not None and q.shape != q_out.shape:
         raise _bad(q_out, "q_out", f"a tensor of q's shape {tuple(q.shape)}")
     for name, t in (("K1", K1), ("V1", V1), ("Ki", Ki), ("Vi", Vi)):
@@ -451,9 +463,10 @@ def yocopp_rope_compose_append(K1, V1, Ki, Vi, alpha: Optional[Sequence[float]],
     rc = (_lib or load()).yocopp_rope_compose_append(
         _rows(K1, "K1", cache, dev, like, n), _rows(V1, "V1", cache, dev, like, n), _rows(Ki, "Ki", cache, dev, like, n),
         _rows(Vi, "Vi", cache, dev, like, n), None if alpha is None else _Float4(*alpha), lam, rope,
-        _ints(positions, "positions", dev, torch.int32), cache, _ints(pos, "pos", dev, torch.int32),
+        _ints(positions, "positions", dev, torch.int32), cache, _ints(pos, "pos", dev, torch.int32, cache.batch),
         _rows(q, "q", cache, dev, like, n), _rows(q_out, "q_out", cache, dev, like, n),
-        q.shape[1] if q is not None else 0, _ints(cu_new, "cu_new", dev, torch.int32), n_uniform, n,
+        q.shape[1] if q is not None else 0, _ints(cu_new, "cu_new", dev, torch.int32, cache.batch + 1),
+        n_uniform, n,
         _raw_stream(stream, dev))
     if rc:
         _check("yocopp_rope_compose_append", rc)
@@ -481,6 +494,8 @@ def alloc_pages_workspace(caches, device=None):
 
 def _pages_refs(caches, refs, dev):
     import torch
+    for c in getattr(caches, "_keep", ())[:1]:
+        _cache_here(c, dev)
     if refs is not None and refs.numel() != caches[0].num_blocks:
         raise _bad(refs, "refs", f"a tensor of {caches[0].num_blocks} counts")
     return _ints(refs, "refs", dev, torch.int32)

@@ -450,7 +450,8 @@ int32_t yocopp_rope_compose_append(const void* K1, const void* V1, const void* K
  * of a model share one block table (the same positions lie in the same blocks
  * of every layer's pool), so these calls take all layers' caches at once:
  * num_caches (1 .. 128) descriptors, HOST array, alike in all but k and v.
- * They WRITE the block table and the pools.
+ * They WRITE the block table and the pools: calls that use the same table or
+ * pools are to be ordered, in one stream or by events.
  *
  *   block_refs : device int32 [num_blocks], how many table entries name the
  *                block; 0 = free.  Zero-filled for an empty pool.

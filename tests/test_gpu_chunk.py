@@ -426,3 +426,26 @@ def test_offsets_past_32_bits(y):
         c.table[0, i] = blocks - 1 - i
     c.cache = y.make_cache(k, v, c.table)
     c.check(y)
+
+
+def test_binding_refuses_what_would_be_read_past_its_end(y):
+    c = Case(y, rows=[3, 4], pos=[10, 20], tree=chain(), seed=23)
+    out = torch.empty_like(c.q)
+    ok = dict(pos=c.pos_t, cu_q=c.cu, max_q=4, tree_mask=c.tree_t)
+    for kw in (dict(pos=c.pos_t[:1]), dict(cu_q=c.cu[:2]), dict(tree_mask=c.tree_t[:6]), dict(total_q=8), dict(num_q_heads=16)):
+        with pytest.raises(TypeError):
+            y.yocopp_chunk_attn(c.q, c.cache, out, c.ws, **{**ok, **kw})
+    with pytest.raises(TypeError):
+        y.yocopp_chunk_attn(c.q, c.cache, out[:, ::2], c.ws, **ok)
+    with pytest.raises(y.YocoppError):
+        y.yocopp_chunk_attn(c.q, c.cache, out, c.ws[: c.ws.numel() - 256], **ok)
+    c.check(y)
+
+
+def test_fewer_rows_than_the_tensor_has(y):
+    c = Case(y, rows=[3, 4], pos=[10, 20], seed=24)
+    big = torch.cat([c.q, c.q])
+    out = torch.full_like(big, 5.0)
+    y.yocopp_chunk_attn(big, c.cache, out, c.ws, pos=c.pos_t, cu_q=c.cu, total_q=7, max_q=4)
+    assert bool((out[7:] == 5).all())
+    c.check(y, out[:7].clone())
