@@ -2,7 +2,8 @@
  * yocopp.h - C ABI of the B200 (sm_100a) YOCO / YOCO++ cross-layer KV cache
  * hot path: the fused residual composition + cache append, and the
  * split-K GQA decode attention that every cross-decoder layer runs over the
- * single shared cache.
+ * single shared cache; and what serving it needs beside them: prefill and chunk
+ * attention, rotary positions, and the pages of paged caches.
  *
  * Conventions for every call:
  *  - All tensor pointers are DEVICE pointers of the current CUDA device,
@@ -535,15 +536,15 @@ int32_t yocopp_set_decode_kernel(int32_t which);
 
 /*
  * yocopp_testing_set_decode_fault - failure-injection hook for tests.
- * Host-side, process-wide; affects later yocopp_decode_attn and
- * yocopp_prefill_attn launches.
+ * Host-side, process-wide; affects later yocopp_decode_attn,
+ * yocopp_prefill_attn and yocopp_chunk_attn launches.
  *   drop_tile     : decode: index (in the split plan's flattened tile order) of
  *                   one tile whose load is never issued, so the consumers' wait
- *                   on it can only run out; prefill: index of the key tile
- *                   whose K load the first CTA never issues; -1 disables the
- *                   injection.
- *   wait_limit_ns : limit of every bounded wait inside the decode and prefill
- *                   kernels (default 2 s); must be > 0.
+ *                   on it can only run out; prefill and chunk: index of the
+ *                   key tile whose K load the first CTA never issues; -1
+ *                   disables the injection.
+ *   wait_limit_ns : limit of every bounded wait inside the decode, prefill and
+ *                   chunk kernels (default 2 s); must be > 0.
  * With a dropped tile the kernel records YOCOPP_ETIMEOUT, waits (bounded) for
  * its own copies still in flight, and returns; the context stays usable.
  * Returns YOCOPP_EINVAL for wait_limit_ns <= 0.
